@@ -1198,19 +1198,18 @@ __global__ void __launch_bounds__(RB_THREADS, 1) chain_bwd_tc_kernel(const BwdAr
                         mma_bf16(tm + 32 * (it & 1), ad + (uint32_t)((kk * 256) >> 4), bd + (uint32_t)((kk * 256) >> 4), id2,
                                  kk > 0 ? 1u : 0u);
                 };
-                // the first chunk's dO image (announced on bar_img's phase 0) and slot
-                if (!mbar_wait(bar_img, 0u, a.status) || !mbar_wait(&bar_ld[bidx(0)], bpar(0), a.status)) {
+                if (!mbar_wait(&bar_ld[bidx(0)], bpar(0), a.status)) {  // the first chunk's slot
                     failed = true;
                 } else {
-                    tc_fence_after();
-                    issue_qdo(0);
                     for (int it = 0; it < nck; ++it) {
-                        // the -dS image of this chunk (and the dO image of the next one)
-                        if (!mbar_wait(bar_img, (uint32_t)((it + 1) & 1), a.status)) {
+                        // the -dS image of this chunk and the dO image of the next one (in
+                        // iteration 0 of the first one too)
+                        if (!mbar_wait(bar_img, (uint32_t)(it & 1), a.status)) {
                             failed = true;
                             break;
                         }
                         tc_fence_after();
+                        if (it == 0) issue_qdo(0);
                         const uint64_t md = sdesc_mn_sw128(sbase + bidx(it) * RB_SLOT + SO_M);
                         const uint64_t sd = sdesc_interleave(sbase + RB_DS, 512u, 128u);
 #pragma unroll
@@ -1269,9 +1268,9 @@ __global__ void __launch_bounds__(RB_THREADS, 1) chain_bwd_tc_kernel(const BwdAr
             load_do(0);
             write_do(0);
             load_do(1);
-            fence_async_smem();
-            tc_fence_before();
-            mbar_arrive(bar_img);
+            // the first dO image is announced with the first -dS image below: each consumer
+            // arrives once per iteration and then waits for that iteration's product, so none
+            // can arrive in a phase before the others have arrived in it
             for (int it = 0; it < nck; ++it) {
                 const int c = nck - 1 - it, b = bidx(it);
                 // dL/d(state at the end of chunk c), as a bf16 operand image (row i, this slice's columns)
