@@ -30,7 +30,7 @@
  *    Errors detected on the device (a bounded wait that expired, cu_seqlens
  *    that contradict T or max_seqlen) are recorded in a status word inside
  *    the workspace and read back with kda_query_status.
- *  - Supported shapes: dk = dv = 128.  Supported dtypes: inputs KDA_F32 or
+ *  - Supported shapes: dk = dv = 128 (the element-wise scan: any D).  Supported dtypes: inputs KDA_F32 or
  *    KDA_BF16 (all of q, k, v, log_alpha, beta, gate share in_dtype);
  *    outputs KDA_F32 or KDA_BF16.  Every pointer must be 16-byte aligned.
  *  - Outputs must not alias inputs, except where stated (in-place states).
@@ -352,6 +352,188 @@ KDA_API kda_status kda_decode_steps(float* state, const void* q, const void* k, 
 KDA_API kda_status kda_gate_norm(const void* o, const void* gate, const float* norm_weight, float eps,
                          void* y, int64_t rows, int dv, kda_dtype in_dtype,
                          kda_dtype out_dtype, void* stream);
+
+/*
+ * Element-wise gated scan: the diagonal relative of the recurrence above, one
+ * state value per channel (no counterpart on the pages).  For every token t of
+ * a sequence and every channel, in fp32:
+ *
+ *     l_t = min(log_alpha_t, 0)            a_t = exp(l_t)
+ *     s_t = sigmoid(gate_t), or 1          w_t = sqrt(1 - a_t^2), or 1
+ *     u_t = w_t * s_t * x_t                h_t = a_t * h_{t-1} + u_t
+ *
+ * log_alpha has no floor here; -inf restarts a channel (a_t = 0).  gate is
+ * optional; `normalize` selects w_t = sqrt(1 - a_t^2), which keeps the state's
+ * variance at the input's.  States are fp32 [N, D].
+ *
+ * Token tensors are [B, T, D] (or packed [1, T, D] with cu_seqlens), channels
+ * contiguous.  The inputs x, log_alpha, gate and d_h take a token stride in
+ * elements (0 = D), so that columns of one wider tensor can be passed as they
+ * lie; they need element alignment only (16-byte aligned pointers with strides
+ * of whole 16 bytes load fastest).  Here and below, cu_seqlens and vectors of
+ * slots need 4-byte alignment, all other pointers 16-byte alignment.  D is any
+ * positive size.
+ *
+ *   cu_seqlens   device int32 [n_seqs + 1], cu[0] = 0, non-decreasing,
+ *                cu[n_seqs] <= T, or NULL for B sequences of T tokens.  Rows of
+ *                tokens at and behind cu[n_seqs] are neither read nor written.
+ *   workspace    NULL, or a buffer whose first word receives the device status
+ *                (kda_query_status): KDA_ERR_DEVICE_ARG when cu_seqlens breaks
+ *                these rules.  Such a call reads and writes nothing out of
+ *                range; its outputs are undefined.  At least
+ *                KDA_STATUS_BYTES when given.
+ */
+#define KDA_STATUS_BYTES 256u
+
+/* Tokens between two rows of chunk_states below. */
+#define KDA_SCAN_CHUNK 64
+
+/*
+ * kda_scan_fwd -- h for every token and the last state of every sequence.
+ *
+ *   x, log_alpha  [B, T, D] in_dtype; gate the same or NULL
+ *   init_state    [N, D] fp32, NULL = zero
+ *   h             [B, T, D] out_dtype, contiguous
+ *   final_state   [N, D] fp32 or NULL; may alias init_state exactly.  The
+ *                 initial state's for a sequence without tokens.
+ *   chunk_states  NULL, or fp32 [ceil(B * T / KDA_SCAN_CHUNK), D]: row c is the
+ *                 state before token c * KDA_SCAN_CHUNK of the B * T tokens in
+ *                 a row (unspecified where a sequence starts there, and at or
+ *                 behind cu[n_seqs]), which kda_scan_bwd takes
+ */
+KDA_API kda_status kda_scan_fwd(const void* x, const void* log_alpha, const void* gate, const float* init_state,
+                                void* h, float* final_state, float* chunk_states, int B, int64_t T, int D,
+                                int64_t x_stride, int64_t log_alpha_stride, int64_t gate_stride,
+                                const int32_t* cu_seqlens, int n_seqs, kda_dtype in_dtype, kda_dtype out_dtype,
+                                int normalize, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_scan_bwd -- gradients of kda_scan_fwd with respect to x, log_alpha, gate
+ * and the initial state, given dL/dh and dL/d(final state):
+ *
+ *     G_t = dh_t + a_{t+1} G_{t+1}   (the last token: + d_final_state)
+ *     dx = G w s;   dgate = G u (1 - s);   d_init = a_first G_first
+ *     dlog_alpha = G (a h_{t-1} - a^2 s x / w)     (second term: normalize)
+ *
+ * The gradient of min(log_alpha, 0) passes where log_alpha <= 0.  The second
+ * term has no limit at log_alpha = 0 (w = 0) and is left out there.
+ *
+ *   x .. init_state, B .. n_seqs, normalize   as kda_scan_fwd
+ *   d_h            [B, T, D] in_dtype; d_final_state [N, D] fp32 or NULL (zero)
+ *   chunk_states   as kda_scan_fwd wrote them for the same arguments, or NULL:
+ *                  then they are computed first, into the workspace
+ *   dx, dlog_alpha, dgate  [B, T, D] grad_dtype, contiguous (dgate NULL without
+ *                  a gate); d_init_state [N, D] fp32 or NULL (for a sequence
+ *                  without tokens d_final_state)
+ *   workspace      kda_scan_bwd_workspace_size bytes when chunk_states is NULL;
+ *                  otherwise as for kda_scan_fwd
+ */
+KDA_API kda_status kda_scan_bwd(const void* x, const void* log_alpha, const void* gate, const float* init_state,
+                                const void* d_h, const float* d_final_state, const float* chunk_states, void* dx,
+                                void* dlog_alpha, void* dgate, float* d_init_state, int B, int64_t T, int D,
+                                int64_t x_stride, int64_t log_alpha_stride, int64_t gate_stride, int64_t d_h_stride,
+                                const int32_t* cu_seqlens, int n_seqs, kda_dtype in_dtype, kda_dtype grad_dtype,
+                                int normalize, void* workspace, size_t workspace_bytes, void* stream);
+
+/* kda_scan_bwd_workspace_size -- the status word and the chunk states of B * T tokens. */
+KDA_API kda_status kda_scan_bwd_workspace_size(int B, int64_t T, int D, size_t* bytes);
+
+/*
+ * kda_scan_decode_steps -- n_steps consecutive tokens of Bd sequences, states in
+ * place (one token per sequence: n_steps = 1).
+ *
+ *   state        [n_slots, D] fp32: row slots[b] is sequence b's state; slots
+ *                NULL: row b (n_slots >= Bd).  Updated in place.
+ *   x, log_alpha, gate  [n_steps, Bd, D] in_dtype contiguous, gate or NULL
+ *   h            [n_steps, Bd, D] out_dtype
+ *   slots        device int32 [Bd] or NULL.  A negative slot, or one of n_slots
+ *                and above, marks a row of padding: its outputs are zeros, its
+ *                inputs are not used and no state changes.  Of rows that name
+ *                the same slot the first is stepped, the others are padding.
+ *   step_states  NULL or [n_steps, Bd, D] fp32: the state after every step
+ *                (rows of padding: zeros)
+ */
+KDA_API kda_status kda_scan_decode_steps(float* state, const void* x, const void* log_alpha, const void* gate, void* h,
+                                         const int32_t* slots, int n_slots, int n_steps, int Bd, int D,
+                                         kda_dtype in_dtype, kda_dtype out_dtype, int normalize, float* step_states,
+                                         void* stream);
+
+/*
+ * kda_decode_steps_paged -- kda_decode_steps for sequences whose states lie in a
+ * pool: state is [n_slots, H, dk, dv] and row b of the batch uses page slots[b]
+ * (slots as for kda_scan_decode_steps; padding: zeros in o and step_states).
+ * A gated call normalises o in fp32, whatever n_steps is.
+ */
+KDA_API kda_status kda_decode_steps_paged(float* state, const int32_t* slots, int n_slots, const void* q,
+                                          const void* k, const void* v, const void* log_alpha, const void* beta,
+                                          void* o, int n_steps, int Bd, int H, int dk, int dv, kda_dtype in_dtype,
+                                          kda_dtype out_dtype, float scale, const void* gate,
+                                          const float* norm_weight, float eps, float* step_states, void* stream);
+
+/*
+ * kda_gate_norm_bwd -- gradients of kda_gate_norm.  With r = (mean(o^2) + eps)^-1/2,
+ * n = o r, s = sigmoid(g):
+ *
+ *     d_gate = dy n w s (1 - s);   d_norm_weight = sum over rows of dy n s
+ *     d_o = r (dn - n mean(dn n)),   dn = dy w s
+ *
+ *   o, gate, d_y  [rows, dv] in_dtype; norm_weight [dv] fp32 or NULL (ones)
+ *   d_o, d_gate   [rows, dv] grad_dtype; d_norm_weight [dv] fp32, or NULL (not
+ *                 wanted).  Sums run in a fixed order: equal inputs give equal bits.
+ *   workspace     kda_gate_norm_bwd_workspace_size bytes, 16-byte aligned; may
+ *                 be NULL when d_norm_weight is
+ */
+KDA_API kda_status kda_gate_norm_bwd(const void* o, const void* gate, const void* d_y, const float* norm_weight,
+                                     float eps, void* d_o, void* d_gate, float* d_norm_weight, int64_t rows, int dv,
+                                     kda_dtype in_dtype, kda_dtype grad_dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+KDA_API kda_status kda_gate_norm_bwd_workspace_size(int64_t rows, int dv, size_t* bytes);
+
+/*
+ * Pages of recurrent states.  A pool is [layers, n_pages, page_bytes]: one page
+ * per sequence slot and layer, the same slot in every layer (prefix cache at
+ * fixed token boundaries, state rollback: the "training and inference systems"
+ * item of the K3 article summaries).
+ *
+ * kda_state_copy -- for i = 0 .. n-1, in list order, in every layer:
+ *     dst page dst_slots[i] = src page src_slots[i],   or zeros when src_slots[i] < 0
+ * with the result of carrying the list out one by one: a page written by one
+ * entry and read by a later one is read as written, and of entries that write
+ * one page the last stands.  An entry whose destination is negative or not
+ * below dst_pages, or whose source is not below src_pages, does nothing.
+ *
+ *   dst, src      device pools, or the same pool twice; they may not overlap in
+ *                 any other way.  src may be NULL when every entry clears.
+ *   page_bytes    a positive multiple of 4; pools 16-byte aligned
+ *   *_layer_bytes distance between layers (layers == 1: ignored); a multiple of
+ *                 4, at least n_pages * page_bytes
+ *   dst_slots, src_slots   device int32 [n]
+ */
+KDA_API kda_status kda_state_copy(void* dst, const void* src, int layers, int64_t page_bytes, int dst_pages,
+                                  int src_pages, int64_t dst_layer_bytes, int64_t src_layer_bytes,
+                                  const int32_t* dst_slots, const int32_t* src_slots, int n, void* stream);
+
+/*
+ * kda_state_alloc -- takes the n lowest free slots: live[p] (one byte per page,
+ * 0 = free) becomes 1 and slots[0 .. n) lists them in rising order, -1 where none
+ * was left.   kda_state_free -- live[slots[i]] = 0; slots out of range are ignored.
+ */
+KDA_API kda_status kda_state_alloc(uint8_t* live, int n_pages, int32_t* slots, int n, void* stream);
+KDA_API kda_status kda_state_free(uint8_t* live, int n_pages, const int32_t* slots, int n, void* stream);
+
+/*
+ * kda_state_compact -- plans the moves that bring all live pages to the front of
+ * the pool: with m live pages, the k-th free slot below m receives the k-th live
+ * page at or above m.  The moves themselves are kda_state_copy(dst_slots,
+ * src_slots, n = n_pages) for each pool that shares the slots.
+ *
+ *   live       [n_pages] bytes, on return 1 for the first m and 0 behind them
+ *   dst_slots, src_slots  int32 [n_pages]: the moves, then -1
+ *   new_slots  int32 [n_pages]: where each old slot's page lies now, -1 if it was free
+ *   n_live     int32 [1]: m
+ */
+KDA_API kda_status kda_state_compact(uint8_t* live, int n_pages, int32_t* dst_slots, int32_t* src_slots,
+                                     int32_t* new_slots, int32_t* n_live, void* stream);
 
 /*
  * kda_query_status -- synchronises `stream`, reads the device status word of

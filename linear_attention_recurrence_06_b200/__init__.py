@@ -16,11 +16,19 @@ Entry points (same names as the C ABI):
   kcp_transition / kcp_compose / kcp_finish
                  the per-device steps of context parallelism across devices
                  (the exchange between them is in ``kcp.py``)
+  scan_fwd / scan_bwd / scan_decode_step(s)
+                 the element-wise gated scan: prefill, gradients, single tokens
+  gate_norm_bwd  gradients of gate_norm
+  state_copy / state_alloc / state_free / state_compact
+                 pages of recurrent states in a pool: copy, fork, clear, take, free
+                 and compact (decode_step(s) and scan_decode_step(s) take `slots`)
   query_status   reads and clears the device status word of a workspace
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +37,7 @@ LIB_PATH = os.path.join(_PKG, "libkda.so")
 KDA_OK = 0
 KDA_F32, KDA_BF16 = 0, 1
 HEAD_DIM = 128
+SCAN_CHUNK = 64  # tokens between two rows of scan_fwd's chunk_states
 
 _STATUS_NAMES = {
     0: "KDA_OK", -1: "KDA_ERR_INVALID_ARG", -2: "KDA_ERR_UNSUPPORTED", -3: "KDA_ERR_MISALIGNED",
@@ -98,6 +107,29 @@ def load_library(path: str | None = None):
                                      vp, vp]
     lib.kda_gate_norm.restype = i32
     lib.kda_gate_norm.argtypes = [vp, vp, vp, f32, vp, i64, i32, i32, i32, vp]
+    ld = [i64] * 3
+    lib.kda_scan_fwd.restype = i32
+    lib.kda_scan_fwd.argtypes = [vp] * 7 + [i32, i64, i32] + ld + [vp, i32, i32, i32, i32, vp, sz, vp]
+    lib.kda_scan_bwd.restype = i32
+    lib.kda_scan_bwd.argtypes = [vp] * 11 + [i32, i64, i32] + ld + [i64, vp, i32, i32, i32, i32, vp, sz, vp]
+    lib.kda_scan_bwd_workspace_size.restype = i32
+    lib.kda_scan_bwd_workspace_size.argtypes = [i32, i64, i32, ctypes.POINTER(sz)]
+    lib.kda_scan_decode_steps.restype = i32
+    lib.kda_scan_decode_steps.argtypes = [vp] * 6 + [i32] * 7 + [vp, vp]
+    lib.kda_decode_steps_paged.restype = i32
+    lib.kda_decode_steps_paged.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp] + [i32] * 7 + [f32, vp, vp, f32, vp, vp]
+    lib.kda_gate_norm_bwd.restype = i32
+    lib.kda_gate_norm_bwd.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, i64, i32, i32, i32, vp, sz, vp]
+    lib.kda_gate_norm_bwd_workspace_size.restype = i32
+    lib.kda_gate_norm_bwd_workspace_size.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    lib.kda_state_copy.restype = i32
+    lib.kda_state_copy.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, vp, vp, i32, vp]
+    lib.kda_state_alloc.restype = i32
+    lib.kda_state_alloc.argtypes = [vp, i32, vp, i32, vp]
+    lib.kda_state_free.restype = i32
+    lib.kda_state_free.argtypes = [vp, i32, vp, i32, vp]
+    lib.kda_state_compact.restype = i32
+    lib.kda_state_compact.argtypes = [vp, i32, vp, vp, vp, vp, vp]
     lib.kda_query_status.restype = i32
     lib.kda_query_status.argtypes = [vp, vp]
     lib.kda_chunk_fwd_noalloc.restype = i32
@@ -370,10 +402,19 @@ def kcp_finish(state_in, workspace, *, shape, dtype, cu_seqlens=None, max_seqlen
 
 
 def decode_step(state, q, k, v, log_alpha, beta, *, scale: float = 1.0, gate=None, norm_weight=None,
-                eps: float = 1e-6, out_dtype=None, out=None, stream=None):
+                eps: float = 1e-6, out_dtype=None, out=None, stream=None, slots=None):
     """One recurrent step.  state: fp32 [Bd, H, 128, 128] (updated in place);
-    q, k, log_alpha, v: [Bd, H, 128]; beta: [Bd, H].  Returns o (or y) [Bd, H, 128]."""
+    q, k, log_alpha, v: [Bd, H, 128]; beta: [Bd, H].  Returns o (or y) [Bd, H, 128].
+    slots: int32 [Bd] on the device: the states lie in a pool [P, H, 128, 128], row b's
+    in page slots[b]; a negative slot marks a row of padding (also one of P and above,
+    and one that an earlier row names): its outputs are zeros and no state changes."""
     torch = _torch()
+    if slots is not None:
+        one = lambda t: None if t is None else t[None]  # noqa: E731
+        o = decode_steps(state, one(q), one(k), one(v), one(log_alpha), one(beta), scale=scale, gate=one(gate),
+                         norm_weight=norm_weight, eps=eps, out_dtype=out_dtype, out=one(out), stream=stream,
+                         slots=slots)
+        return out if out is not None else o[0]
     _check_cuda(state, q, k, v, log_alpha, beta, gate, norm_weight)
     if state.dtype != torch.float32:
         raise TypeError("state must be fp32")
@@ -390,13 +431,17 @@ def decode_step(state, q, k, v, log_alpha, beta, *, scale: float = 1.0, gate=Non
 
 
 def decode_steps(state, q, k, v, log_alpha, beta, *, scale: float = 1.0, gate=None, norm_weight=None,
-                 eps: float = 1e-6, out_dtype=None, out=None, step_states=None, stream=None):
+                 eps: float = 1e-6, out_dtype=None, out=None, step_states=None, stream=None, slots=None):
     """n consecutive recurrent steps in one call (e.g. verifying n draft tokens).
     state: fp32 [Bd, H, 128, 128], carried through the steps in place;
     q, k, log_alpha, v: [n, Bd, H, 128]; beta: [n, Bd, H].  step_states: None,
     True (allocate) or an fp32 [n, Bd, H, 128, 128] tensor that receives the state
-    after every step.  Returns o (or y) [n, Bd, H, 128], or (o, step_states) when
-    step_states was requested."""
+    after every step.  slots: as decode_step (state is then a pool of pages; with a
+    gate, o is normalised in fp32 whatever n is).  Returns o (or y) [n, Bd, H, 128], or
+    (o, step_states) when step_states was requested."""
+    if slots is not None:
+        return _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, norm_weight, eps, out_dtype,
+                                   out, step_states, stream)
     torch = _torch()
     want = step_states is not None
     if step_states is True:
@@ -417,6 +462,40 @@ def decode_steps(state, q, k, v, log_alpha, beta, *, scale: float = 1.0, gate=No
     return (o, step_states) if want else o
 
 
+def _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, norm_weight, eps, out_dtype, out,
+                        step_states, stream):
+    torch = _torch()
+    _check_cuda(q)
+    if q.dim() != 4:
+        raise ValueError("q must be [n, Bd, H, 128]")
+    n, Bd, H, dk = q.shape
+    dv = v.shape[-1]
+    rows = (n, Bd, H)
+    _check_like(q, torch.float32, (state.shape[0], H, dk, dv), "state", state)
+    _check_slots(q, slots, "slots", Bd)
+    for t, shape, name in ((k, rows + (dk,), "k"), (v, rows + (dv,), "v"), (log_alpha, rows + (dk,), "log_alpha"),
+                           (beta, rows, "beta"), (gate, rows + (dv,), "gate")):
+        _check_like(q, q.dtype, shape, name, t)
+    _check_like(q, torch.float32, (dv,), "norm_weight", norm_weight)
+    odt = out_dtype if out_dtype is not None else (q.dtype if out is None else out.dtype)
+    want = step_states is not None
+    with _on(q, stream):
+        o = out if out is not None else torch.empty(rows + (dv,), dtype=odt, device=q.device)
+        if step_states is True:
+            step_states = torch.empty(rows + (dk, dv), dtype=torch.float32, device=q.device)
+        if out is not None:
+            _check_like(q, odt, rows + (dv,), "out", out)
+        if want:
+            _check_like(q, torch.float32, rows + (dk, dv), "step_states", step_states)
+        st = load_library().kda_decode_steps_paged(_ptr(state), _ptr(slots), state.shape[0], _ptr(q), _ptr(k), _ptr(v),
+                                                   _ptr(log_alpha), _ptr(beta), _ptr(o), n, Bd, H, dk, dv, _dt(q),
+                                                   _dt(o), float(scale), _ptr(gate), _ptr(norm_weight), float(eps),
+                                                   _ptr(step_states), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_decode_steps_paged")
+    return (o, step_states) if want else o
+
+
 def gate_norm(o, g, norm_weight=None, *, eps: float = 1e-6, out_dtype=None, out=None, stream=None):
     """y = o / sqrt(mean(o^2) + eps) * w * sigmoid(g) over the last dim (128)."""
     torch = _torch()
@@ -430,6 +509,338 @@ def gate_norm(o, g, norm_weight=None, *, eps: float = 1e-6, out_dtype=None, out=
     if st != KDA_OK:
         raise KdaError(st, "kda_gate_norm")
     return y
+
+
+def _on(t, stream):
+    """Context in which a call on tensor t runs: its device current, and `stream`
+    (of that device) the current stream, so that what the call allocates belongs to it."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _check_like(x, dtype, shape, name, t):
+    """t: a contiguous tensor of this dtype and shape on x's device."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != x.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {x.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_slots(x, slots, name, n=None):
+    torch = _torch()
+    if slots is None:
+        return
+    if not slots.is_cuda or slots.device != x.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {x.device}")
+    if slots.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if slots.dim() != 1 or (n is not None and slots.numel() != n) or not slots.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector" + (f" of {n}" if n is not None else ""))
+
+
+def _token_rows(x, t, name):
+    """Token stride (elements) of a scan input [B, T, ...] whose channels lie together."""
+    if t.device != x.device or not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
+    if t.dtype != x.dtype:
+        raise TypeError("x, log_alpha, gate and d_h must share one dtype")
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have x's shape {tuple(x.shape)}, not {tuple(t.shape)}")
+    if t.is_contiguous() or t.numel() == 0:
+        return 0
+    D = 1
+    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if size > 1 and stride != D:
+            raise ValueError(f"{name}: the channels of a token must lie together")
+        D *= size
+    B, T = t.shape[0], t.shape[1]
+    row = t.stride(1) if T > 1 else t.stride(0) if B > 1 else D
+    if row < D or (B > 1 and T > 1 and t.stride(0) != T * row):
+        raise ValueError(f"{name}: tokens must lie at one distance of at least a token's channels")
+    return row
+
+
+def _scan_dims(x, cu_seqlens, initial_state):
+    torch = _torch()
+    if not x.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    if x.dim() < 3:
+        raise ValueError("x must be [B, T, D] (or [B, T, H, d])")
+    B, T = x.shape[0], x.shape[1]
+    ch = tuple(x.shape[2:])
+    N = B
+    if cu_seqlens is not None:
+        _check_slots(x, cu_seqlens, "cu_seqlens")
+        N = cu_seqlens.numel() - 1
+    _check_like(x, torch.float32, (N,) + ch, "initial_state", initial_state)
+    return B, T, ch, math.prod(ch), N
+
+
+def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = False, cu_seqlens=None, out_dtype=None,
+             output_final_state: bool = True, final_state=None, out=None, chunk_states=None, workspace=None,
+             stream=None):
+    """Element-wise gated scan: h_t = a_t h_{t-1} + w_t sigmoid(gate_t) x_t with
+    a_t = exp(min(log_alpha_t, 0)), and w_t = sqrt(1 - a_t^2) if normalize else 1.
+
+    x, log_alpha, gate: [B, T, D] or [B, T, H, d] (bf16 or fp32, one dtype; gate
+    optional: factor 1).  They may be column slices of wider tensors: the channels of
+    a token lie together, the tokens at one distance.  initial_state: fp32 [N, D]
+    ([N, H, d]) or None.  Varlen: B = 1 and cu_seqlens int32 [N+1] on the device;
+    rows of tokens behind cu_seqlens[N] are left as they are.
+    Returns (h, final_state fp32 [N, D] or None); with chunk_states (True: allocate)
+    also those, for scan_bwd.  workspace: optional, for query_status."""
+    torch = _torch()
+    B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
+    ld = [_token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha"),
+          0 if gate is None else _token_rows(x, gate, "gate")]
+    odt = out_dtype if out_dtype is not None else (x.dtype if out is None else out.dtype)
+    n_chunks = -(-B * T // SCAN_CHUNK)
+    with _on(x, stream):
+        h = out if out is not None else torch.empty(x.shape, dtype=odt, device=x.device)
+        fs = final_state
+        if fs is None and output_final_state:
+            fs = torch.empty((N,) + ch, dtype=torch.float32, device=x.device)
+        want = chunk_states is not None
+        if chunk_states is True:
+            chunk_states = torch.empty((n_chunks,) + ch, dtype=torch.float32, device=x.device)
+        if out is not None:
+            _check_like(x, odt, x.shape, "out", out)
+        if final_state is not None:
+            _check_like(x, torch.float32, (N,) + ch, "final_state", fs)
+        if want:
+            _check_like(x, torch.float32, (n_chunks,) + ch, "chunk_states", chunk_states)
+        _check_cuda(workspace)
+        st = load_library().kda_scan_fwd(_ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(initial_state), _ptr(h), _ptr(fs),
+                                         _ptr(chunk_states), B, T, D, *ld, _ptr(cu_seqlens), N, _dt(x), _dt(h),
+                                         int(normalize), _ptr(workspace),
+                                         0 if workspace is None else workspace.numel(), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_scan_fwd")
+    return (h, fs, chunk_states) if want else (h, fs)
+
+
+def scan_bwd_workspace_size(B: int, T: int, D: int) -> int:
+    """Workspace bytes of scan_bwd without chunk_states."""
+    n = ctypes.c_size_t(0)
+    st = load_library().kda_scan_bwd_workspace_size(B, T, D, ctypes.byref(n))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_scan_bwd_workspace_size")
+    return n.value
+
+
+def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=None, normalize: bool = False,
+             cu_seqlens=None, chunk_states=None, out_dtype=None, want_d_initial_state: bool = True, workspace=None,
+             stream=None):
+    """Gradients of scan_fwd: inputs as there, d_h = dL/dh (x's dtype and shape),
+    d_final_state = dL/d(final state) fp32 [N, D] or None.  chunk_states: what
+    scan_fwd(chunk_states=True) returned for the same inputs; without them they are
+    computed first.  Returns a dict: dx, dlog_alpha, dgate (x's shape, fp32 or
+    out_dtype; dgate None without a gate) and d_initial_state fp32 [N, D] (None when
+    not wanted)."""
+    torch = _torch()
+    B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
+    ld = [_token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha"),
+          0 if gate is None else _token_rows(x, gate, "gate"), _token_rows(x, d_h, "d_h")]
+    _check_like(x, torch.float32, (N,) + ch, "d_final_state", d_final_state)
+    _check_like(x, torch.float32, (-(-B * T // SCAN_CHUNK),) + ch, "chunk_states", chunk_states)
+    odt = out_dtype if out_dtype is not None else torch.float32
+    with _on(x, stream):
+        g = {k: torch.empty(x.shape, dtype=odt, device=x.device) for k in ("dx", "dlog_alpha")}
+        g["dgate"] = None if gate is None else torch.empty(x.shape, dtype=odt, device=x.device)
+        g["d_initial_state"] = torch.empty((N,) + ch, dtype=torch.float32, device=x.device) \
+            if want_d_initial_state else None
+        if workspace is None and chunk_states is None:
+            workspace = torch.empty(scan_bwd_workspace_size(B, T, D), dtype=torch.uint8, device=x.device)
+        _check_cuda(workspace)
+        st = load_library().kda_scan_bwd(_ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(initial_state), _ptr(d_h),
+                                         _ptr(d_final_state), _ptr(chunk_states), _ptr(g["dx"]),
+                                         _ptr(g["dlog_alpha"]), _ptr(g["dgate"]), _ptr(g["d_initial_state"]), B, T, D,
+                                         *ld, _ptr(cu_seqlens), N, _dt(x), _dt(g["dx"]), int(normalize),
+                                         _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_scan_bwd")
+    return g
+
+
+def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False, slots=None, out_dtype=None, out=None,
+                      step_states=None, stream=None):
+    """n consecutive tokens of the element-wise gated scan for Bd sequences.
+    x, log_alpha, gate: [n, Bd, D] ([n, Bd, H, d]); state: fp32 [P, D], updated in
+    place: sequence b's is row slots[b] (int32 [Bd]; None: row b).  A negative slot
+    marks a row of padding (also one of P and above, and one that an earlier row
+    names): its outputs are zeros and no state changes.  step_states: None, True
+    (allocate) or fp32 [n, Bd, D] receiving the state after every token.
+    Returns h [n, Bd, D], or (h, step_states)."""
+    torch = _torch()
+    _check_cuda(state, x, log_alpha, gate)
+    if x.dim() < 3:
+        raise ValueError("x must be [n, Bd, D] (or [n, Bd, H, d])")
+    for t, name in ((log_alpha, "log_alpha"), (gate, "gate")):
+        _check_like(x, x.dtype, x.shape, name, t)
+    n, Bd = x.shape[0], x.shape[1]
+    ch = tuple(x.shape[2:])
+    _check_like(x, torch.float32, (state.shape[0],) + ch, "state", state)
+    _check_slots(x, slots, "slots", Bd)
+    odt = out_dtype if out_dtype is not None else (x.dtype if out is None else out.dtype)
+    want = step_states is not None
+    with _on(x, stream):
+        h = out if out is not None else torch.empty(x.shape, dtype=odt, device=x.device)
+        if step_states is True:
+            step_states = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        if out is not None:
+            _check_like(x, odt, x.shape, "out", out)
+        if want:
+            _check_like(x, torch.float32, x.shape, "step_states", step_states)
+        st = load_library().kda_scan_decode_steps(_ptr(state), _ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(h),
+                                                  _ptr(slots), state.shape[0], n, Bd, math.prod(ch), _dt(x), _dt(h),
+                                                  int(normalize), _ptr(step_states), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_scan_decode_steps")
+    return (h, step_states) if want else h
+
+
+def scan_decode_step(state, x, log_alpha, *, gate=None, normalize: bool = False, slots=None, out_dtype=None, out=None,
+                     stream=None):
+    """scan_decode_steps for one token: x, log_alpha, gate [Bd, D]; returns h [Bd, D]."""
+    one = lambda t: None if t is None else t[None]  # noqa: E731
+    h = scan_decode_steps(state, one(x), one(log_alpha), gate=one(gate), normalize=normalize, slots=slots,
+                          out_dtype=out_dtype, out=one(out), stream=stream)
+    return out if out is not None else h[0]
+
+
+def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=None,
+                  want_d_norm_weight: bool = True, workspace=None, stream=None):
+    """Gradients of gate_norm: o, g and d_y = dL/dy [..., 128] of one dtype.  Returns a dict:
+    d_o, d_gate (o's shape, fp32 or out_dtype) and d_norm_weight fp32 [128] (None when not
+    wanted; without a norm_weight the gradient at a weight of ones)."""
+    torch = _torch()
+    _check_cuda(o, g, d_y, norm_weight, workspace)
+    if o.shape[-1] != HEAD_DIM:
+        raise KdaError(-2, "kda_gate_norm_bwd")
+    for t, name in ((g, "g"), (d_y, "d_y")):
+        _check_like(o, o.dtype, o.shape, name, t)
+    _check_like(o, torch.float32, (HEAD_DIM,), "norm_weight", norm_weight)
+    rows = o.numel() // HEAD_DIM
+    odt = out_dtype if out_dtype is not None else torch.float32
+    with _on(o, stream):
+        r = dict(d_o=torch.empty(o.shape, dtype=odt, device=o.device),
+                 d_gate=torch.empty(o.shape, dtype=odt, device=o.device),
+                 d_norm_weight=torch.empty(HEAD_DIM, dtype=torch.float32, device=o.device)
+                 if want_d_norm_weight else None)
+        if workspace is None and want_d_norm_weight:
+            n = ctypes.c_size_t(0)
+            st = load_library().kda_gate_norm_bwd_workspace_size(rows, HEAD_DIM, ctypes.byref(n))
+            if st != KDA_OK:
+                raise KdaError(st, "kda_gate_norm_bwd_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=o.device)
+        st = load_library().kda_gate_norm_bwd(_ptr(o), _ptr(g), _ptr(d_y), _ptr(norm_weight), float(eps),
+                                              _ptr(r["d_o"]), _ptr(r["d_gate"]), _ptr(r["d_norm_weight"]), rows,
+                                              HEAD_DIM, _dt(o), _dt(r["d_o"]), _ptr(workspace),
+                                              0 if workspace is None else workspace.numel(), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_gate_norm_bwd")
+    return r
+
+
+def _pool_dims(t, layered, name):
+    """(layers, pages, bytes of a page, bytes between layers) of a pool [P, ...] or [L, P, ...]."""
+    lead = 2 if layered else 1
+    if t.dim() < lead:
+        raise ValueError(f"{name} must be [{'layers, ' if layered else ''}pages, ...]")
+    page = math.prod(t.shape[lead:]) * t.element_size()
+    L, P = (t.shape[0], t.shape[1]) if layered else (1, t.shape[0])
+    inner = t[0] if layered and L > 0 else t
+    if not inner.is_contiguous():
+        raise ValueError(f"the pages of {name} must be contiguous, one behind the other")
+    return L, P, page, t.stride(0) * t.element_size() if layered else 0
+
+
+def state_copy(dst, dst_slots, src, src_slots, *, layered: bool = False, stream=None):
+    """Copies pages of recurrent states: for each i in list order, dst[dst_slots[i]] =
+    src[src_slots[i]], or zeros where src_slots[i] < 0.  dst, src: pools [P, ...] of one
+    dtype and page shape (or one pool twice); layered: [L, P, ...], the same slots in
+    every layer.  Slots are int32 vectors on the device; an entry with a negative
+    destination, or a slot out of range, does nothing.  The result is that of carrying
+    the list out one by one.  src None: every entry clears.  Returns dst."""
+    if not dst.is_cuda or (src is not None and (not src.is_cuda or src.device != dst.device)):
+        raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
+    _check_slots(dst, dst_slots, "dst_slots")
+    _check_slots(dst, src_slots, "src_slots", dst_slots.numel())
+    L, P, page, d_layer = _pool_dims(dst, layered, "dst")
+    Q, s_layer = 0, 0
+    if src is not None:
+        if src.dtype != dst.dtype or src.shape[1 + layered:] != dst.shape[1 + layered:] or \
+                (layered and src.shape[0] != L):
+            raise ValueError("dst and src must have one dtype, page shape and number of layers")
+        _, Q, _, s_layer = _pool_dims(src, layered, "src")
+    if page == 0:
+        return dst
+    with _on(dst, stream):
+        st = load_library().kda_state_copy(_ptr(dst), _ptr(src), L, page, P, Q, d_layer, s_layer, _ptr(dst_slots),
+                                           _ptr(src_slots), dst_slots.numel(), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_copy")
+    return dst
+
+
+def _check_live(live):
+    torch = _torch()
+    _check_cuda(live)
+    if live.dtype not in (torch.uint8, torch.bool) or live.dim() != 1:
+        raise TypeError("live must be a vector of uint8 or bool, one per page")
+
+
+def state_alloc(live, n: int, *, stream=None):
+    """Takes the n lowest free slots of a pool: marks them in live (uint8 or bool [P], on the
+    device) and returns them as int32 [n], -1 where no slot was left."""
+    torch = _torch()
+    _check_live(live)
+    with _on(live, stream):
+        slots = torch.empty(n, dtype=torch.int32, device=live.device)
+        st = load_library().kda_state_alloc(_ptr(live), live.numel(), _ptr(slots), n, _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_alloc")
+    return slots
+
+
+def state_free(live, slots, *, stream=None):
+    """Marks slots (int32, on the device; those out of range are ignored) free in live."""
+    _check_live(live)
+    _check_slots(live, slots, "slots")
+    with _on(live, stream):
+        st = load_library().kda_state_free(_ptr(live), live.numel(), _ptr(slots), slots.numel(), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_free")
+
+
+def state_compact(live, *, stream=None):
+    """Plans the moves that bring the live pages of a pool to its front and updates live.
+    Returns a dict of int32 tensors: dst_slots, src_slots [P] (the moves, then -1: pass
+    both to state_copy with the pool twice, for every pool that shares the slots),
+    new_slots [P] (where each old slot's page lies now, -1 if free) and n_live [1]."""
+    torch = _torch()
+    _check_live(live)
+    P = live.numel()
+    with _on(live, stream):
+        r = {k: torch.empty(P, dtype=torch.int32, device=live.device) for k in ("dst_slots", "src_slots", "new_slots")}
+        r["n_live"] = torch.empty(1, dtype=torch.int32, device=live.device)
+        st = load_library().kda_state_compact(_ptr(live), P, _ptr(r["dst_slots"]), _ptr(r["src_slots"]),
+                                              _ptr(r["new_slots"]), _ptr(r["n_live"]), _stream(None))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_compact")
+    return r
 
 
 def query_status(workspace, stream=None) -> int:

@@ -11,6 +11,7 @@
 #include "../../include/kda.h"
 #include "kda_launch.h"
 #include "kda_profile.h"
+#include "kda_scan.h"
 
 
 namespace kda {
@@ -63,6 +64,7 @@ namespace {
 constexpr int kSupportedD = 128;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }  // vectors of slots
 bool dtype_ok(int d) { return d == KDA_F32 || d == KDA_BF16; }
 
 int num_sms_cached() {
@@ -303,10 +305,11 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, const void
     return from_cuda(e);
 }
 
-kda_status kda_decode_steps(float* state, const void* q, const void* k, const void* v, const void* log_alpha,
-                            const void* beta, void* o, int n_steps, int Bd, int H, int dk, int dv,
-                            kda_dtype in_dtype, kda_dtype out_dtype, float scale, const void* gate,
-                            const float* norm_weight, float eps, float* step_states, void* stream) {
+static kda_status decode_steps_impl(float* state, const int32_t* slots, int n_slots, const void* q, const void* k,
+                                    const void* v, const void* log_alpha, const void* beta, void* o, int n_steps,
+                                    int Bd, int H, int dk, int dv, kda_dtype in_dtype, kda_dtype out_dtype,
+                                    float scale, const void* gate, const float* norm_weight, float eps,
+                                    float* step_states, void* stream) {
     if (!state || !q || !k || !v || !log_alpha || !beta || !o) return KDA_ERR_INVALID_ARG;
     if (n_steps < 0 || Bd < 0 || H <= 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype) || eps < 0.f)
         return KDA_ERR_INVALID_ARG;
@@ -315,14 +318,37 @@ kda_status kda_decode_steps(float* state, const void* q, const void* k, const vo
     const void* ptrs[] = {state, q, k, v, log_alpha, beta, o, gate, norm_weight, step_states};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (!aligned4(slots)) return KDA_ERR_MISALIGNED;
     if (Bd == 0 || n_steps == 0) return KDA_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     kda::prof_begin(kda::PROF_DECODE, st);
-    const cudaError_t e = kda::launch_decode_step(state, q, k, v, log_alpha, beta, o, Bd, H, in_dtype == KDA_BF16,
-                                                  out_dtype == KDA_BF16, scale, gate, norm_weight, eps, n_steps,
-                                                  step_states, st);
+    const cudaError_t e =
+        slots ? kda::launch_decode_paged(state, slots, n_slots, q, k, v, log_alpha, beta, o, Bd, H,
+                                         in_dtype == KDA_BF16, out_dtype == KDA_BF16, scale, gate, norm_weight, eps,
+                                         n_steps, step_states, st)
+              : kda::launch_decode_step(state, q, k, v, log_alpha, beta, o, Bd, H, in_dtype == KDA_BF16,
+                                        out_dtype == KDA_BF16, scale, gate, norm_weight, eps, n_steps, step_states,
+                                        st);
     kda::prof_end(kda::PROF_DECODE, st);
     return from_cuda(e);
+}
+
+kda_status kda_decode_steps(float* state, const void* q, const void* k, const void* v, const void* log_alpha,
+                            const void* beta, void* o, int n_steps, int Bd, int H, int dk, int dv,
+                            kda_dtype in_dtype, kda_dtype out_dtype, float scale, const void* gate,
+                            const float* norm_weight, float eps, float* step_states, void* stream) {
+    return decode_steps_impl(state, nullptr, 0, q, k, v, log_alpha, beta, o, n_steps, Bd, H, dk, dv, in_dtype,
+                             out_dtype, scale, gate, norm_weight, eps, step_states, stream);
+}
+
+kda_status kda_decode_steps_paged(float* state, const int32_t* slots, int n_slots, const void* q, const void* k,
+                                  const void* v, const void* log_alpha, const void* beta, void* o, int n_steps, int Bd,
+                                  int H, int dk, int dv, kda_dtype in_dtype, kda_dtype out_dtype, float scale,
+                                  const void* gate, const float* norm_weight, float eps, float* step_states,
+                                  void* stream) {
+    if (!slots || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    return decode_steps_impl(state, slots, n_slots, q, k, v, log_alpha, beta, o, n_steps, Bd, H, dk, dv, in_dtype,
+                             out_dtype, scale, gate, norm_weight, eps, step_states, stream);
 }
 
 kda_status kda_decode_step(float* state, const void* q, const void* k, const void* v, const void* log_alpha,
@@ -350,6 +376,227 @@ kda_status kda_gate_norm(const void* o, const void* gate, const float* norm_weig
     return from_cuda(e);
 }
 
+}  // extern "C"
+
+namespace {
+
+// token strides: 0 stands for D
+bool scan_strides(int D, int64_t* a, int64_t* b, int64_t* c, int64_t* d) {
+    int64_t* const all[] = {a, b, c, d};
+    for (int64_t* s : all) {
+        if (!s) continue;
+        if (*s == 0) *s = D;
+        if (*s < D) return false;
+    }
+    return true;
+}
+
+bool element_aligned(const void* p, kda_dtype t) {
+    return (reinterpret_cast<uintptr_t>(p) & (t == KDA_BF16 ? 1u : 3u)) == 0;
+}
+
+// The checks that the scan's two directions share.  Fills in n_seqs for a batch of equal lengths.
+kda_status scan_check(const kda::ScanArgs& a, kda_dtype in_dtype, kda_dtype out_dtype, int* n_seqs, size_t ws_need,
+                      const void* workspace, size_t workspace_bytes) {
+    if (a.B <= 0 || a.T < 0 || a.D <= 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return KDA_ERR_INVALID_ARG;
+    if (a.T > 0 && (!a.x || !a.log_alpha)) return KDA_ERR_INVALID_ARG;
+    if (a.cu) {
+        if (a.B != 1 || *n_seqs <= 0) return KDA_ERR_INVALID_ARG;
+        if (a.T > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    } else {
+        *n_seqs = a.B;
+    }
+    if (a.T > (int64_t(1) << 40) / a.B) return KDA_ERR_UNSUPPORTED;
+    const void* in[] = {a.x, a.log_alpha, a.gate, a.d_h};
+    for (const void* p : in)
+        if (p && !element_aligned(p, in_dtype)) return KDA_ERR_MISALIGNED;
+    const void* ptrs[] = {a.init, a.h, a.final_state, a.chunk_states, a.d_final, a.dx, a.dl, a.dg, a.d_init};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (!aligned4(a.cu)) return KDA_ERR_MISALIGNED;
+    if (workspace || ws_need) {
+        if (!workspace || workspace_bytes < (ws_need ? ws_need : KDA_STATUS_BYTES)) return KDA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return KDA_ERR_MISALIGNED;
+    }
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_scan_fwd(const void* x, const void* log_alpha, const void* gate, const float* init_state, void* h,
+                        float* final_state, float* chunk_states, int B, int64_t T, int D, int64_t x_stride,
+                        int64_t log_alpha_stride, int64_t gate_stride, const int32_t* cu_seqlens, int n_seqs,
+                        kda_dtype in_dtype, kda_dtype out_dtype, int normalize, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    if (!scan_strides(D, &x_stride, &log_alpha_stride, &gate_stride, nullptr)) return KDA_ERR_INVALID_ARG;
+    kda::ScanArgs a{};
+    a.x = x, a.log_alpha = log_alpha, a.gate = gate;
+    a.ld_x = x_stride, a.ld_l = log_alpha_stride, a.ld_g = gate_stride;
+    a.init = init_state, a.cu = cu_seqlens, a.B = B, a.D = D, a.T = T;
+    a.in_bf16 = in_dtype == KDA_BF16, a.out_bf16 = out_dtype == KDA_BF16, a.normalize = normalize != 0;
+    a.status = static_cast<uint32_t*>(workspace);
+    a.h = h, a.final_state = final_state, a.chunk_states = chunk_states;
+    const kda_status st = scan_check(a, in_dtype, out_dtype, &n_seqs, 0, workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
+    if (T > 0 && !h) return KDA_ERR_INVALID_ARG;
+    a.n_seqs = n_seqs;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    kda::prof_begin(kda::PROF_SCAN, s);
+    const cudaError_t e = kda::launch_scan_fwd(a, s);
+    kda::prof_end(kda::PROF_SCAN, s);
+    return from_cuda(e);
+}
+
+kda_status kda_scan_bwd_workspace_size(int B, int64_t T, int D, size_t* bytes) {
+    if (B <= 0 || T < 0 || D <= 0 || !bytes) return KDA_ERR_INVALID_ARG;
+    if (T > (int64_t(1) << 40) / B) return KDA_ERR_UNSUPPORTED;
+    const size_t chunks = (size_t)(((int64_t)B * T + KDA_SCAN_CHUNK - 1) / KDA_SCAN_CHUNK);
+    *bytes = KDA_STATUS_BYTES + chunks * (size_t)D * sizeof(float);
+    return KDA_OK;
+}
+
+kda_status kda_scan_bwd(const void* x, const void* log_alpha, const void* gate, const float* init_state,
+                        const void* d_h, const float* d_final_state, const float* chunk_states, void* dx,
+                        void* dlog_alpha, void* dgate, float* d_init_state, int B, int64_t T, int D, int64_t x_stride,
+                        int64_t log_alpha_stride, int64_t gate_stride, int64_t d_h_stride, const int32_t* cu_seqlens,
+                        int n_seqs, kda_dtype in_dtype, kda_dtype grad_dtype, int normalize, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    if (!scan_strides(D, &x_stride, &log_alpha_stride, &gate_stride, &d_h_stride)) return KDA_ERR_INVALID_ARG;
+    kda::ScanArgs a{};
+    a.x = x, a.log_alpha = log_alpha, a.gate = gate, a.d_h = d_h;
+    a.ld_x = x_stride, a.ld_l = log_alpha_stride, a.ld_g = gate_stride, a.ld_dh = d_h_stride;
+    a.init = init_state, a.cu = cu_seqlens, a.B = B, a.D = D, a.T = T;
+    a.in_bf16 = in_dtype == KDA_BF16, a.out_bf16 = grad_dtype == KDA_BF16, a.normalize = normalize != 0;
+    a.status = static_cast<uint32_t*>(workspace);
+    a.chunk_states = const_cast<float*>(chunk_states);
+    a.d_final = d_final_state, a.dx = dx, a.dl = dlog_alpha, a.dg = dgate, a.d_init = d_init_state;
+    size_t need = 0;
+    if (B > 0 && T >= 0 && D > 0 && !chunk_states) {
+        const kda_status st = kda_scan_bwd_workspace_size(B, T, D, &need);
+        if (st != KDA_OK) return st;
+    }
+    const kda_status st = scan_check(a, in_dtype, grad_dtype, &n_seqs, need, workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
+    if (T > 0 && (!d_h || !dx || !dlog_alpha || (gate != nullptr) != (dgate != nullptr))) return KDA_ERR_INVALID_ARG;
+    a.n_seqs = n_seqs;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool own_states = !chunk_states;
+    if (own_states)
+        a.chunk_states = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
+    kda::prof_begin(kda::PROF_SCAN_BWD, s);
+    const cudaError_t e = kda::launch_scan_bwd(a, own_states, s);
+    kda::prof_end(kda::PROF_SCAN_BWD, s);
+    return from_cuda(e);
+}
+
+kda_status kda_scan_decode_steps(float* state, const void* x, const void* log_alpha, const void* gate, void* h,
+                                 const int32_t* slots, int n_slots, int n_steps, int Bd, int D, kda_dtype in_dtype,
+                                 kda_dtype out_dtype, int normalize, float* step_states, void* stream) {
+    if (n_steps < 0 || Bd < 0 || D <= 0 || n_slots < 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype))
+        return KDA_ERR_INVALID_ARG;
+    if (Bd == 0 || n_steps == 0) return KDA_OK;
+    if (!state || !x || !log_alpha || !h || (!slots && n_slots < Bd)) return KDA_ERR_INVALID_ARG;
+    if (Bd > 65535) return KDA_ERR_UNSUPPORTED;  // grid y extent
+    const void* ptrs[] = {state, x, log_alpha, gate, h, step_states};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (!aligned4(slots)) return KDA_ERR_MISALIGNED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    kda::prof_begin(kda::PROF_SCAN_DECODE, s);
+    const cudaError_t e =
+        kda::launch_scan_decode(state, x, log_alpha, gate, h, slots, n_slots, n_steps, Bd, D, in_dtype == KDA_BF16,
+                                out_dtype == KDA_BF16, normalize != 0, step_states, s);
+    kda::prof_end(kda::PROF_SCAN_DECODE, s);
+    return from_cuda(e);
+}
+
+kda_status kda_gate_norm_bwd_workspace_size(int64_t rows, int dv, size_t* bytes) {
+    if (rows < 0 || !bytes) return KDA_ERR_INVALID_ARG;
+    if (dv != kSupportedD) return KDA_ERR_UNSUPPORTED;
+    *bytes = (size_t)kda::gate_norm_bwd_blocks(rows) * dv * sizeof(float);
+    return KDA_OK;
+}
+
+kda_status kda_gate_norm_bwd(const void* o, const void* gate, const void* d_y, const float* norm_weight, float eps,
+                             void* d_o, void* d_gate, float* d_norm_weight, int64_t rows, int dv, kda_dtype in_dtype,
+                             kda_dtype grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || !dtype_ok(in_dtype) || !dtype_ok(grad_dtype) || !(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (rows > 0 && (!o || !gate || !d_y || !d_o || !d_gate)) return KDA_ERR_INVALID_ARG;
+    if (dv != kSupportedD) return KDA_ERR_UNSUPPORTED;
+    const void* ptrs[] = {o, gate, d_y, norm_weight, d_o, d_gate, d_norm_weight, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    size_t need = 0;
+    const kda_status st = kda_gate_norm_bwd_workspace_size(rows, dv, &need);
+    if (st != KDA_OK) return st;
+    if (d_norm_weight && need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    kda::prof_begin(kda::PROF_GATE_NORM_BWD, s);
+    const cudaError_t e = kda::launch_gate_norm_bwd(o, gate, d_y, norm_weight, eps, d_o, d_gate, d_norm_weight, rows,
+                                                    in_dtype == KDA_BF16, grad_dtype == KDA_BF16,
+                                                    static_cast<float*>(workspace), s);
+    kda::prof_end(kda::PROF_GATE_NORM_BWD, s);
+    return from_cuda(e);
+}
+
+kda_status kda_state_copy(void* dst, const void* src, int layers, int64_t page_bytes, int dst_pages, int src_pages,
+                          int64_t dst_layer_bytes, int64_t src_layer_bytes, const int32_t* dst_slots,
+                          const int32_t* src_slots, int n, void* stream) {
+    if (layers < 0 || n < 0 || page_bytes <= 0 || page_bytes % 4 != 0 || dst_pages < 0 || src_pages < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (n == 0 || layers == 0 || dst_pages == 0) return KDA_OK;
+    if (!dst || !dst_slots || !src_slots || (!src && src_pages > 0)) return KDA_ERR_INVALID_ARG;
+    if (layers > 65535 || n > 65535 || page_bytes > (int64_t(1) << 40)) return KDA_ERR_UNSUPPORTED;  // grid extents
+    if (!aligned16(dst) || !aligned16(src) || !aligned4(dst_slots) || !aligned4(src_slots)) return KDA_ERR_MISALIGNED;
+    const int64_t d_size = page_bytes * dst_pages, s_size = page_bytes * src_pages;
+    if (layers == 1) dst_layer_bytes = d_size, src_layer_bytes = s_size;
+    if (dst_layer_bytes < d_size || src_layer_bytes < s_size || dst_layer_bytes % 4 != 0 || src_layer_bytes % 4 != 0)
+        return KDA_ERR_INVALID_ARG;
+    if (src_pages > 0) {
+        // one pool twice, or two that share no byte
+        const uintptr_t d0 = (uintptr_t)dst, s0 = (uintptr_t)src;
+        const uintptr_t d1 = d0 + (uintptr_t)(dst_layer_bytes * (layers - 1) + d_size);
+        const uintptr_t s1 = s0 + (uintptr_t)(src_layer_bytes * (layers - 1) + s_size);
+        const bool one = d0 == s0 && (layers == 1 || dst_layer_bytes == src_layer_bytes);
+        if (!one && d0 < s1 && s0 < d1) return KDA_ERR_INVALID_ARG;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    kda::prof_begin(kda::PROF_PAGES, s);
+    const cudaError_t e = kda::launch_state_copy(dst, src, layers, page_bytes, dst_pages, src_pages, dst_layer_bytes,
+                                                 src_layer_bytes, dst_slots, src_slots, n, s);
+    kda::prof_end(kda::PROF_PAGES, s);
+    return from_cuda(e);
+}
+
+kda_status kda_state_alloc(uint8_t* live, int n_pages, int32_t* slots, int n, void* stream) {
+    if (n < 0 || n_pages < 0) return KDA_ERR_INVALID_ARG;
+    if (n == 0) return KDA_OK;
+    if ((!live && n_pages > 0) || !slots) return KDA_ERR_INVALID_ARG;
+    if (!aligned4(slots)) return KDA_ERR_MISALIGNED;
+    return from_cuda(kda::launch_state_alloc(live, n_pages, slots, n, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_state_free(uint8_t* live, int n_pages, const int32_t* slots, int n, void* stream) {
+    if (n < 0 || n_pages < 0) return KDA_ERR_INVALID_ARG;
+    if (n == 0 || n_pages == 0) return KDA_OK;
+    if (!live || !slots) return KDA_ERR_INVALID_ARG;
+    if (!aligned4(slots)) return KDA_ERR_MISALIGNED;
+    return from_cuda(kda::launch_state_free(live, n_pages, slots, n, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_state_compact(uint8_t* live, int n_pages, int32_t* dst_slots, int32_t* src_slots, int32_t* new_slots,
+                             int32_t* n_live, void* stream) {
+    if (n_pages < 0 || !n_live) return KDA_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!live || !dst_slots || !src_slots || !new_slots)) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {dst_slots, src_slots, new_slots, n_live};
+    for (const void* p : ptrs)
+        if (!aligned4(p)) return KDA_ERR_MISALIGNED;
+    return from_cuda(kda::launch_state_compact(live, n_pages, dst_slots, src_slots, new_slots, n_live,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
 kda_status kda_profile_enable(int on) {
     kda::g_prof_on = on != 0;
     return KDA_OK;
@@ -358,7 +605,9 @@ kda_status kda_profile_enable(int on) {
 kda_status kda_profile_read(kda_kernel_time* out, int max_entries, int* n_entries) {
     static const char* names[kda::PROF_KINDS] = {"intra",      "chain",    "gate_norm",
                                                  "decode",     "check_cu", "kcp_compose",
-                                                 "chain_bwd",  "intra_bwd"};
+                                                 "chain_bwd",  "intra_bwd", "scan",
+                                                 "scan_bwd",   "scan_decode", "gate_norm_bwd",
+                                                 "pages"};
     int launches[kda::PROF_KINDS] = {0};
     double ms[kda::PROF_KINDS] = {0};
     kda_status st = KDA_OK;

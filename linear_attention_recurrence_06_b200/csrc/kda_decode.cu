@@ -9,9 +9,24 @@
 // and o = scale * (S'^T q + (k . q) u), so both dot products over the key
 // channels come from ONE pass over S' and the state is read and written once.
 #include "kda_launch.h"
+#include "kda_row_slot.cuh"
 #include "kda_sm100.cuh"
 
 namespace kda {
+
+// What a row of padding gets in a paged call: zeros in columns [c0, c0 + nc) of its
+// outputs and of its states after every step.
+template <bool OUT_BF16, int THREADS>
+__device__ __noinline__ void zero_row(void* o, float* step_states, int n_steps, size_t BH, int bh, int c0, int nc) {
+    constexpr int D = 128;
+    for (int t = 0; t < n_steps; ++t) {
+        const size_t tb = (size_t)t * BH + bh;
+        for (int c = threadIdx.x; c < nc; c += THREADS) st_out<OUT_BF16>(o, tb * D + c0 + c, 0.f);
+        if (step_states)
+            for (int i = threadIdx.x; i < D * nc; i += THREADS)
+                step_states[tb * D * D + (size_t)(i / nc) * D + c0 + i % nc] = 0.f;
+    }
+}
 
 // One CTA = one (sequence, head) state [128 x 128] fp32 = 64 KiB, carried
 // through n_steps consecutive tokens; the state is read once and written once
@@ -25,13 +40,14 @@ namespace kda {
 // r0 + 8i (i = 0..15) x 4 columns = 64 fp32 registers.
 // Token tensors are step-major: element (step t, sequence-head bh, channel c)
 // at (t * BH + bh) * 128 + c (beta: t * BH + bh).
-template <bool IN_BF16, bool OUT_BF16, bool GATE>
+// PAGED: the states lie in a pool, row b's in page slots[b]; rows of padding get zeros.
+template <bool IN_BF16, bool OUT_BF16, bool GATE, bool PAGED>
 __global__ void __launch_bounds__(256, 2)
 decode_step_kernel(float* __restrict__ state, const void* __restrict__ q, const void* __restrict__ k,
                    const void* __restrict__ v, const void* __restrict__ log_alpha,
                    const void* __restrict__ beta, void* __restrict__ o, const void* __restrict__ gate,
                    const float* __restrict__ norm_w, float scale, float eps, int n_steps,
-                   float* __restrict__ step_states) {
+                   float* __restrict__ step_states, const int32_t* __restrict__ slots, int n_slots, int H) {
     constexpr int D = 128;
     const int bh = blockIdx.x;  // sequence * H + head
     const size_t BH = gridDim.x;
@@ -44,7 +60,16 @@ decode_step_kernel(float* __restrict__ state, const void* __restrict__ q, const 
     __shared__ float s_k[2][D], s_q[2][D], s_alpha[2][D];
     __shared__ float s_ss[2][8];
 
-    float* S = state + (size_t)bh * D * D;
+    size_t page = bh;  // of one head
+    if constexpr (PAGED) {
+        const int slot = row_slot(slots, n_slots, bh / H);
+        if (slot < 0) {
+            zero_row<OUT_BF16, 256>(o, step_states, n_steps, BH, bh, 0, D);
+            return;
+        }
+        page = (size_t)slot * H + bh % H;
+    }
+    float* S = state + page * D * D;
     float4 st[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -182,11 +207,12 @@ KDA_DEV void cp_async16(void* smem_dst, const void* gmem_src) {
 KDA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 KDA_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-template <bool IN_BF16, bool OUT_BF16>
+template <bool IN_BF16, bool OUT_BF16, bool PAGED>
 __global__ void __launch_bounds__(128, 4)
 decode_multi_kernel(float* __restrict__ state, const void* __restrict__ q, const void* __restrict__ k,
                     const void* __restrict__ v, const void* __restrict__ log_alpha, const void* __restrict__ beta,
-                    void* __restrict__ o, float scale, int n_steps, float* __restrict__ step_states) {
+                    void* __restrict__ o, float scale, int n_steps, float* __restrict__ step_states,
+                    const int32_t* __restrict__ slots, int n_slots, int H) {
     constexpr int D = 128;
     const int bh = blockIdx.x >> 1, sl = blockIdx.x & 1;  // (sequence * H + head, column half)
     const size_t BH = gridDim.x >> 1;
@@ -233,9 +259,18 @@ decode_multi_kernel(float* __restrict__ state, const void* __restrict__ q, const
         // beta of step t0 + tid: kept in a register until the block's wait
         return tid < nb ? ld_in<IN_BF16>(beta, (size_t)(t0 + tid) * BH + bh) : 0.f;
     };
+    size_t page = bh;  // of one head
+    if constexpr (PAGED) {
+        const int slot = row_slot(slots, n_slots, bh / H);
+        if (slot < 0) {
+            zero_row<OUT_BF16, 128>(o, step_states, n_steps, BH, bh, 64 * sl, 64);
+            return;
+        }
+        page = (size_t)slot * H + bh % H;
+    }
     float beta_next = fetch_block(0);  // in flight with the state load
 
-    float* S = state + (size_t)bh * D * D;
+    float* S = state + page * D * D;
     float2 st[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) st[i] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)(row0 + i) * D + col));
@@ -419,8 +454,8 @@ cudaError_t launch_decode_step(float* state, const void* q, const void* k, const
     if (g && n_steps == 1) {  // one step with the gate fused: one CTA per (sequence, head)
         const dim3 grid((unsigned)((int64_t)Bd * H)), block(256);
 #define KDA_DEC(IB, OB)                                                                                    \
-    decode_step_kernel<IB, OB, true><<<grid, block, 0, stream>>>(state, q, k, v, log_alpha, beta, o, gate, \
-                                                                 norm_w, scale, eps, n_steps, step_states)
+    decode_step_kernel<IB, OB, true, false><<<grid, block, 0, stream>>>(                                   \
+        state, q, k, v, log_alpha, beta, o, gate, norm_w, scale, eps, n_steps, step_states, nullptr, 0, H)
         if (in_bf16) { if (out_bf16) KDA_DEC(true, true); else KDA_DEC(true, false); }
         else         { if (out_bf16) KDA_DEC(false, true); else KDA_DEC(false, false); }
 #undef KDA_DEC
@@ -430,8 +465,8 @@ cudaError_t launch_decode_step(float* state, const void* q, const void* k, const
     // then run over the n_steps output rows in place
     const dim3 grid((unsigned)((int64_t)Bd * H * 2)), block(128);
 #define KDA_DECM(IB, OB)                                                                               \
-    decode_multi_kernel<IB, OB><<<grid, block, 0, stream>>>(state, q, k, v, log_alpha, beta, o, scale, \
-                                                            n_steps, step_states)
+    decode_multi_kernel<IB, OB, false><<<grid, block, 0, stream>>>(state, q, k, v, log_alpha, beta, o, \
+                                                                   scale, n_steps, step_states, nullptr, 0, H)
     if (in_bf16) { if (out_bf16) KDA_DECM(true, true); else KDA_DECM(true, false); }
     else         { if (out_bf16) KDA_DECM(false, true); else KDA_DECM(false, false); }
 #undef KDA_DECM
@@ -442,6 +477,25 @@ cudaError_t launch_decode_step(float* state, const void* q, const void* k, const
     if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
     return launch_gate_norm(o, gate, norm_w, eps, o, (int64_t)n_steps * Bd * H, out_bf16, in_bf16, out_bf16, sms,
                             stream);
+}
+
+cudaError_t launch_decode_paged(float* state, const int32_t* slots, int n_slots, const void* q, const void* k,
+                                const void* v, const void* log_alpha, const void* beta, void* o, int Bd, int H,
+                                bool in_bf16, bool out_bf16, float scale, const void* gate, const float* norm_w,
+                                float eps, int n_steps, float* step_states, cudaStream_t stream) {
+    // with a gate: whole heads, the norm and gate fused into every step, so that a row of
+    // padding is finished by the CTA that knows it as one
+#define KDA_DECP(IB, OB)                                                                                          \
+    if (gate)                                                                                                     \
+        decode_step_kernel<IB, OB, true, true><<<(unsigned)((int64_t)Bd * H), 256, 0, stream>>>(                  \
+            state, q, k, v, log_alpha, beta, o, gate, norm_w, scale, eps, n_steps, step_states, slots, n_slots, H); \
+    else                                                                                                          \
+        decode_multi_kernel<IB, OB, true><<<(unsigned)((int64_t)Bd * H * 2), 128, 0, stream>>>(                   \
+            state, q, k, v, log_alpha, beta, o, scale, n_steps, step_states, slots, n_slots, H)
+    if (in_bf16) { if (out_bf16) { KDA_DECP(true, true); } else { KDA_DECP(true, false); } }
+    else         { if (out_bf16) { KDA_DECP(false, true); } else { KDA_DECP(false, false); } }
+#undef KDA_DECP
+    return cudaGetLastError();
 }
 
 cudaError_t launch_gate_norm(const void* o, const void* g, const float* norm_w, float eps, void* y,

@@ -18,6 +18,11 @@ cudaError_t launch_decode_step(float* state, const void* q, const void* k, const
                                const void* beta, void* o, int Bd, int H, bool in_bf16, bool out_bf16, float scale,
                                const void* gate, const float* norm_w, float eps, int n_steps, float* step_states,
                                cudaStream_t stream);
+// The same for rows whose states are pages of a pool: row b uses page slots[b].
+cudaError_t launch_decode_paged(float* state, const int32_t* slots, int n_slots, const void* q, const void* k,
+                                const void* v, const void* log_alpha, const void* beta, void* o, int Bd, int H,
+                                bool in_bf16, bool out_bf16, float scale, const void* gate, const float* norm_w,
+                                float eps, int n_steps, float* step_states, cudaStream_t stream);
 cudaError_t launch_gate_norm(const void* o, const void* g, const float* norm_w, float eps, void* y, int64_t rows,
                              bool o_bf16, bool g_bf16, bool out_bf16, int num_sms, cudaStream_t stream);
 size_t chunk_slot_bytes();
@@ -50,5 +55,20 @@ cudaError_t chunk_bwd_launch(const void* q, const void* k, const void* v, const 
                              float* dv, float* dlog_alpha, float* dbeta, float* d_init, int B, int64_t T, int H,
                              const int32_t* cu, int n_seqs, int64_t max_seqlen, bool in_bf16, float scale,
                              void* workspace, size_t fwd_bytes, cudaStream_t stream);
+
+// Gradients of the gate norm; `partial`: gate_norm_bwd_blocks(rows) x 128 floats when dw is wanted.
+int gate_norm_bwd_blocks(int64_t rows);
+cudaError_t launch_gate_norm_bwd(const void* o, const void* g, const void* dy, const float* w, float eps, void* d_o,
+                                 void* d_g, float* dw, int64_t rows, bool in_bf16, bool out_bf16, float* partial,
+                                 cudaStream_t stream);
+
+// Pages of recurrent states.
+cudaError_t launch_state_copy(void* dst, const void* src, int layers, int64_t page_bytes, int dst_pages, int src_pages,
+                              int64_t dst_layer, int64_t src_layer, const int32_t* dst_slots,
+                              const int32_t* src_slots, int n, cudaStream_t stream);
+cudaError_t launch_state_compact(uint8_t* live, int P, int32_t* dst_slots, int32_t* src_slots, int32_t* new_slots,
+                                 int32_t* n_live, cudaStream_t stream);
+cudaError_t launch_state_alloc(uint8_t* live, int P, int32_t* slots, int n, cudaStream_t stream);
+cudaError_t launch_state_free(uint8_t* live, int P, const int32_t* slots, int n, cudaStream_t stream);
 
 }  // namespace kda
