@@ -19,8 +19,31 @@ struct ScanTerm {
     float s;   // sigmoid(gate), 1 without a gate
 };
 
-// l = min(log_alpha, 0) that keeps NaN
-KDA_DEV float scan_clamp(float log_alpha) { return log_alpha > 0.f ? 0.f : log_alpha; }
+// The hardware's approximations without their denormal handling (results below 2^-126 are 0).
+KDA_DEV float ex2_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+KDA_DEV float rcp_ftz(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+KDA_DEV float rsqrt_ftz(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+KDA_DEV float exp_ftz(float x) { return ex2_ftz(x * LOG2E); }
+
+// l = min(log_alpha, 0), NaN kept
+KDA_DEV float scan_clamp(float log_alpha) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(log_alpha), "f"(0.f));
+    return r;
+}
 
 KDA_DEV float scan_decay(float l) {
     // e^l - 1 for l in (-1/4, 0]: its Taylor polynomial to l^6 (the next term is
@@ -30,7 +53,7 @@ KDA_DEV float scan_decay(float l) {
     t = fmaf(t, l, 1.f / 6.f);
     t = fmaf(t, l, 0.5f);
     const float em = fmaf(t * l, l, l);
-    const float e = __expf(l);
+    const float e = exp_ftz(l);
     return l > SCAN_SLOW ? __uint_as_float(__float_as_uint(em) | 0x80000000u) : e;
 }
 
@@ -50,11 +73,11 @@ template <bool GATE, bool NORM>
 KDA_DEV ScanTerm scan_term(float x, float log_alpha, float g) {
     ScanTerm r;
     r.p = scan_decay(scan_clamp(log_alpha));
-    r.s = GATE ? __fdividef(1.f, 1.f + __expf(-g)) : 1.f;
+    r.s = GATE ? rcp_ftz(1.f + exp_ftz(-g)) : 1.f;
     r.ws = r.s;
     if (NORM) {
         const float n = scan_one_minus_a2(r.p);
-        r.ws *= n * rsqrtf(fmaxf(n, SCAN_TINY));
+        r.ws *= n * rsqrt_ftz(fmaxf(n, SCAN_TINY));
     }
     r.u = r.ws * x;
     return r;
