@@ -402,11 +402,10 @@ kda_status scan_check(const kda::ScanArgs& a, kda_dtype in_dtype, kda_dtype out_
     if (a.T > 0 && (!a.x || !a.log_alpha)) return KDA_ERR_INVALID_ARG;
     if (a.cu) {
         if (a.B != 1 || *n_seqs <= 0) return KDA_ERR_INVALID_ARG;
-        if (a.T > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     } else {
         *n_seqs = a.B;
     }
-    if (a.T > (int64_t(1) << 40) / a.B) return KDA_ERR_UNSUPPORTED;
+    if (a.T > kda::SCAN_MAX_TOKENS / a.B) return KDA_ERR_UNSUPPORTED;
     const void* in[] = {a.x, a.log_alpha, a.gate, a.d_h};
     for (const void* p : in)
         if (p && !element_aligned(p, in_dtype)) return KDA_ERR_MISALIGNED;
@@ -451,7 +450,7 @@ kda_status kda_scan_fwd(const void* x, const void* log_alpha, const void* gate, 
 
 kda_status kda_scan_bwd_workspace_size(int B, int64_t T, int D, size_t* bytes) {
     if (B <= 0 || T < 0 || D <= 0 || !bytes) return KDA_ERR_INVALID_ARG;
-    if (T > (int64_t(1) << 40) / B) return KDA_ERR_UNSUPPORTED;
+    if (T > kda::SCAN_MAX_TOKENS / B) return KDA_ERR_UNSUPPORTED;
     const size_t chunks = (size_t)(((int64_t)B * T + KDA_SCAN_CHUNK - 1) / KDA_SCAN_CHUNK);
     *bytes = KDA_STATUS_BYTES + chunks * (size_t)D * sizeof(float);
     return KDA_OK;

@@ -1,5 +1,7 @@
 // kda_scan.cu -- element-wise gated scan (include/kda.h, kda_scan_fwd), forward
 // and single tokens.
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "kda_row_slot.cuh"
@@ -8,167 +10,241 @@
 
 namespace kda {
 
+bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, bool bf16) {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encoder{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder.load(std::memory_order_relaxed);
+    if (!enc) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return false;
+        enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        encoder.store(enc, std::memory_order_relaxed);
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
+    const cuuint32_t box[2] = {SC_CH, (cuuint32_t)(bf16 ? ScanGeo<true>::NT : ScanGeo<false>::NT)}, one[2] = {1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
+               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
-// The forward: kda_scan_tile.cuh says how the work is split.  Two tiles of a CTA are in
-// flight while it computes on a third's registers; a warp loads and reads only its own
-// rows, so that one barrier per tile remains, between the warps' pieces and their fold.
-template <bool BF16, bool GATE, bool NORM>
+// The forward: kda_scan_tile.cuh says how the work is split.  A warp's first run keeps each token's
+// state from zero and the product of the decays up to it; with the state before the warp's
+// tokens known, the second is one fused product per value.  (Those products' rounding stays
+// inside a token's output; what is carried on goes by the sum of the log-decays.)
+template <bool BF16, bool GATE>
 struct ScanFwd {
-    static constexpr int NT = BF16 ? 16 : 8;
-    using Geo = ScanGeo<BF16, NT>;
+    using Geo = ScanGeo<BF16>;
     static constexpr int N_IN = GATE ? 3 : 2;
-    static constexpr int STAGE = N_IN * Geo::TENS;
-    static constexpr int OFF_AB = 2 * STAGE;                              // [2][warps][32] float4
-    static constexpr int OFF_EX = OFF_AB + 2 * SC_WARPS * 32 * 16;        // [2][cluster][32] float4
-    static constexpr int OFF_TAB = OFF_EX + 2 * SC_MAX_CLUSTER * 32 * 16; // [warps][2][NT] int
-    static constexpr int SMEM = OFF_TAB + SC_WARPS * 2 * NT * 4;
-    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+    static constexpr int ROWS = Geo::NT * Geo::ROWB;                         // a warp's rows of one tensor
+    static constexpr int STAGE = N_IN * ROWS;                                // [warps][2] stages
+    static constexpr int OFF_AB = SC_WARPS * 2 * STAGE;                      // [2][warps][32] pieces up to a warp
+    static constexpr int OFF_BAR = OFF_AB + 2 * SC_WARPS * 512;              // full[warps][2], given[warps][2], sent[4][cluster]
+    static constexpr int OFF_EX = OFF_BAR + (4 * SC_WARPS + 4 * SC_MAX_CLUSTER) * 8;  // [4][cluster][32] the CTAs' pieces
+    static constexpr int smem(int cluster) { return OFF_EX + 4 * cluster * 512; }
+    static_assert(2 * (OFF_EX + 4 * 4 * 512 + 1024) <= 228 * 1024, "two CTAs per SM with clusters up to 4");
 };
 
 template <bool BF16, bool GATE, bool NORM>
-__global__ void __launch_bounds__(SC_THREADS, 2) scan_fwd_kernel(const ScanArgs a, int cluster, int width) {
-    using K = ScanFwd<BF16, GATE, NORM>;
-    using Geo = typename K::Geo;
-    constexpr int NT = K::NT, TILE = Geo::TILE;
+__global__ void __launch_bounds__(SC_THREADS, 2)
+scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
+    using K = ScanFwd<BF16, GATE>;
+    using Geo = ScanGeo<BF16>;
+    constexpr int NT = Geo::NT, TILE = Geo::TILE;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % cluster, ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
     const ScanSpan sp = scan_span(a, blockIdx.y, gridDim.y, lane);
-    const int64_t tile0 = sp.t0 / TILE, n_tiles = sp.t1 > sp.t0 ? (sp.t1 + TILE - 1) / TILE - tile0 : 0;
-    const int64_t n_steps = (n_tiles + cluster - 1) / cluster;
-    float4* const s_ab = reinterpret_cast<float4*>(smem + K::OFF_AB);
-    float4* const s_ex = reinterpret_cast<float4*>(smem + K::OFF_EX);
-    int* const tab = reinterpret_cast<int*>(smem + K::OFF_TAB) + warp * 2 * NT;
-    int ptr = sp.n0;
-    const bool even = (D & 1) == 0;
+    const int tile0 = sp.t0 / TILE, n_tiles = sp.t1 > sp.t0 ? (sp.t1 + TILE - 1) / TILE - tile0 : 0;
+    const int n_steps = (n_tiles + cluster - 1) / cluster;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + K::OFF_BAR);
+    uint64_t* const full = bars + 2 * warp;                    // this warp's loads
+    uint64_t* const given = bars + 2 * SC_WARPS + 2 * warp;    // this warp's piece
+    uint64_t* const sent = bars + 4 * SC_WARPS;                // the cluster's pieces, [4][cluster]
+    float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);
+    uint8_t* const stages = smem + warp * 2 * K::STAGE;
+    const bool even = (D & 1) == 0, tma = width == 16;
+    bool failed = false;
 
-    auto first_token = [&](int64_t s) { return (tile0 + s * cluster + rank) * TILE + warp * NT; };
-    auto load = [&](int64_t s) {
-        if (s < n_steps) {
-            uint8_t* st = smem + (s & 1) * K::STAGE;
-            const int64_t tw = first_token(s);
-            load_rows<BF16, NT>(st, a.log_alpha, a.ld_l, tw, sp.t0, sp.t1, ch0, D, width, warp, lane);
-            load_rows<BF16, NT>(st + Geo::TENS, a.x, a.ld_x, tw, sp.t0, sp.t1, ch0, D, width, warp, lane);
-            if (GATE)
-                load_rows<BF16, NT>(st + 2 * Geo::TENS, a.gate, a.ld_g, tw, sp.t0, sp.t1, ch0, D, width, warp, lane);
-        }
-        cp_commit();
-    };
-    load(0);
-    load(1);
-    if (cluster > 1) {  // every CTA of the cluster runs before another writes into its shared memory
-        cluster_arrive();
-        cluster_wait();
+    if (tma && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4 * SC_WARPS + 4 * cluster; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        if (cluster > 1)
+            for (int i = 0; i < 4 * cluster; ++i) mbar_arrive_expect_tx(&sent[i], 512);
     }
+    __syncthreads();
+    int tw = (tile0 + rank) * TILE + warp * NT;
+    const int by = cluster * TILE;
+    auto load = [&](int s, int t) {  // step s, whose tokens begin at t
+        uint8_t* const st = stages + (s & 1) * K::STAGE;
+        if (tma) {
+            if (lane == 0 && s < n_steps) {
+                uint64_t* const b = full + (s & 1);
+                mbar_arrive_expect_tx(b, K::STAGE);
+                tma_load_2d(st, &maps.m[0], ch0, t, b);
+                tma_load_2d(st + K::ROWS, &maps.m[1], ch0, t, b);
+                if (GATE) tma_load_2d(st + 2 * K::ROWS, &maps.m[2], ch0, t, b);
+            }
+        } else {
+            if (s < n_steps) {
+                load_rows<BF16>(st, a.log_alpha, a.ld_l, t, sp.t0, sp.t1, ch0, D, width, lane);
+                load_rows<BF16>(st + K::ROWS, a.x, a.ld_x, t, sp.t0, sp.t1, ch0, D, width, lane);
+                if (GATE) load_rows<BF16>(st + 2 * K::ROWS, a.gate, a.ld_g, t, sp.t0, sp.t1, ch0, D, width, lane);
+            }
+            cp_commit();
+        }
+    };
+    load(0, tw);
+    load(1, tw + by);
+    if (cluster > 1) cluster_sync_all();  // every CTA's barriers are set up before another writes to them
 
-    float2 carry = f2(0.f);  // the state before the cluster's tiles of this step
-    for (int64_t s = 0; s < n_steps; ++s) {
-        const int64_t tw = first_token(s);
-        const ScanBounds<NT> bd = scan_bounds<NT>(a, sp, tw, &ptr, tab, lane);
-        cp_wait<1>();
-        __syncwarp();
-        const uint8_t* st = smem + (s & 1) * K::STAGE;
+    ScanSeen at;
+    at.calm = 0;
+    float2 carry = f2(0.f);  // the state before this CTA's tile
+    for (int s = 0; s < n_steps; ++s, tw += by) {
+        float4* const ab = reinterpret_cast<float4*>(smem + K::OFF_AB) + (s & 1) * (SC_WARPS * 32);
+        if (s >= at.calm) at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
+        const uint32_t phase = (s >> 1) & 1;
+        if (tma) {
+            failed = failed || !mbar_wait(full + (s & 1), phase, a.status);
+        } else {
+            cp_wait<1>();
+            __syncwarp();
+        }
+        const uint8_t* const st = stages + (s & 1) * K::STAGE;
 
-        // the warp's piece, from zero
-        float2 e[NT], u[NT], sum = f2(0.f), h = f2(0.f);
-        uint32_t lo[NT];
-        auto piece = [&](auto has_starts) {
+        // the warp's tokens from zero: states h, products of the decays A
+        float2 hs[NT], as[NT], sum = f2(0.f);
+        // whole rows, and sequences meet at most before the first token and behind the last
+        const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
+        float2 h0 = f2(0.f);
+        if (at.starts & 1) {
+            const int n = at.seq_start(0);
+            if (a.init) h0 = load2(a.init, n, D, ch);
+        }
+        auto first_run = [&](auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const float2 la = tile_at<BF16>(st, warp * NT + i, lane);
-                const float2 x = tile_at<BF16>(st + Geo::TENS, warp * NT + i, lane);
-                const float2 g = GATE ? tile_at<BF16>(st + 2 * Geo::TENS, warp * NT + i, lane) : f2(0.f);
-                const float2 l = f2(scan_clamp(la.x), scan_clamp(la.y));
-                const ScanDecay2 d = scan_decay2(l);
-                float2 sg;
-                u[i] = GATE || NORM ? __fmul2_rn(scan_weight2<GATE, NORM>(d.em, g, &sg), x) : x;
-                e[i] = d.e;
-                lo[i] = pack_bf16x2(d.lo.x, d.lo.y);
-                sum = __fadd2_rn(sum, l);
-                if (decltype(has_starts)::value && (bd.starts >> i & 1)) {  // the first token's state takes u's place
-                    const float2 h0 = a.init ? load2(a.init, (size_t)bd.seq_start(i), D, ch) : f2(0.f);
-                    u[i] = h = scan_step2(d.e, d.lo, h0, u[i]);
+                float2 d = scan_depth2(tile_at<BF16>(st, i, lane)), u = tile_at<BF16>(st + K::ROWS, i, lane);
+                const float2 g = GATE ? tile_at<BF16>(st + 2 * K::ROWS, i, lane) : f2(0.f);
+                const bool own = !EDGE || (at.own >> i & 1);
+                if (!own) d = f2(0.f);
+                const ScanDecay2 a2 = scan_decay2(d);
+                if (GATE || NORM) u = __fmul2_rn(scan_weight2<GATE, NORM>(a2.m, g), u);
+                if (!own) u = f2(0.f);
+                sum = __fadd2_rn(sum, d);
+                if (i == 0) {
+                    hs[0] = u;
+                    as[0] = __fadd2_rn(a2.e, a2.lo);
                 } else {
-                    h = scan_step2(d.e, d.lo, h, u[i]);
+                    hs[i] = scan_step2(a2.e, a2.lo, hs[i - 1], u);
+                    as[i] = __ffma2_rn(a2.lo, as[i - 1], __fmul2_rn(a2.e, as[i - 1]));
+                }
+                if (EDGE && i > 0 && (at.starts >> i & 1)) {
+                    const int n = at.seq_start(i);
+                    hs[i] = scan_step2(a2.e, a2.lo, a.init ? load2(a.init, n, D, ch) : f2(0.f), u);
                 }
             }
         };
-        if (bd.starts) piece(std::true_type{});
-        else piece(std::false_type{});
+        if (plain) first_run(std::false_type{});
+        else first_run(std::true_type{});
+        float4 piece = scan_piece(false, sum, hs[NT - 1]);
+        if (at.starts) {  // nothing of what came before gets through
+            const float2 b = at.starts == 1 ? scan_fold2(piece, h0) : hs[NT - 1];
+            piece = make_float4(SC_CUT, SC_CUT, b.x, b.y);
+        }
         __syncwarp();
-        load(s + 2);  // into the stage that this warp has just read
-        float4* const ab = s_ab + (s & 1) * (SC_WARPS * 32);
-        const bool cut = bd.starts != 0;
-        ab[warp * 32 + lane] = make_float4(cut ? SCAN_CUT : scan_decay(sum.x), cut ? SCAN_CUT : scan_decay(sum.y), h.x, h.y);
-        __syncthreads();
+        if (!failed) load(s + 2, tw + 2 * by);  // into the stage that this warp has just read
 
-        // the state before this warp's tokens, and the carry of the next step
-        float2 mine = carry;
-        if (cluster > 1) {
-            float4* const ex = s_ex + (s & 1) * (SC_MAX_CLUSTER * 32);
-            if (warp == 0) {
-                float4 all = ab[lane];
-#pragma unroll
-                for (int w = 1; w < SC_WARPS; ++w) all = scan_join(all, ab[w * 32 + lane]);
-                const uint32_t at = smem_u32(ex + rank * 32 + lane);
-                for (int c = 0; c < cluster; ++c) st_cluster(map_to_cta(at, c), all);
-            }
-            cluster_arrive();
-            cluster_wait();
-            for (int c = 0; c < cluster; ++c) {
-                if (c == rank) mine = carry;
-                carry = scan_fold2(ex[c * 32 + lane], carry);
-            }
-            for (int w = 0; w < warp; ++w) mine = scan_fold2(ab[w * 32 + lane], mine);
+        // the pieces of the warps before it; its own joined to them goes on
+        float4 before = make_float4(-0.f, -0.f, 0.f, 0.f);
+        if (warp > 0) {
+            failed = failed || !mbar_wait(given - 2 + (s & 1), phase, a.status);
+            before = ab[(warp - 1) * 32 + lane];
+            piece = scan_join2(before, piece);
+        }
+        if (warp < SC_WARPS - 1) {
+            ab[warp * 32 + lane] = piece;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(given + (s & 1));
         } else {
-#pragma unroll
-            for (int w = 0; w < SC_WARPS; ++w) {
-                if (w == warp) mine = carry;
-                carry = scan_fold2(ab[w * 32 + lane], carry);
+            // Four buffers: a CTA that sends for step s + 4 has folded all pieces of step s + 2, whose
+            // warps are done with step s + 1, in which they read the pieces of step s last.
+            const int slot = (s & 3) * cluster + rank;
+            if (cluster > 1) {
+                const uint32_t to = smem_u32(ex + slot * 32 + lane), on = smem_u32(sent + slot);
+                for (int c = 0; c < cluster; ++c) st_async16(map_to_cta(to, c), piece, map_to_cta(on, c));
+            } else {
+                ex[slot * 32 + lane] = piece;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sent + slot);
             }
         }
 
-        if (a.chunk_states && tw % SCAN_CHUNK == 0 && tw >= sp.t0 && tw < sp.t1) {
+        // the state before this CTA's tile: its own and the later CTAs' pieces of the last step,
+        // the earlier ones' of this step; then the state before this warp's tokens
+        for (int k = 0; k < cluster; ++k) {
+            const bool last = rank + k < cluster;
+            const int c = last ? rank + k : rank + k - cluster, q = last ? s - 1 : s, slot = (q & 3) * cluster + c;
+            if (q < 0) continue;
+            const uint32_t ph = (q >> 2) & 1;
+            failed = failed || !(cluster > 1 ? mbar_wait_peers(sent + slot, ph, a.status) : mbar_wait(sent + slot, ph, a.status));
+            if (cluster > 1 && warp == 0 && lane == 0) mbar_arrive_expect_tx(sent + slot, 512);  // for step q + 4
+            const float4 v = ex[slot * 32 + lane];
+            carry = scan_fold2(v, carry, scan_is_cut(v));
+        }
+        float2 mine = warp > 0 ? scan_fold2(before, carry, scan_is_cut(before)) : carry;
+        if (at.starts & 1) mine = h0;
+
+        if (warp % (SCAN_CHUNK / NT) == 0 && a.chunk_states && tw >= sp.t0 && tw < sp.t1) {
             const size_t i = (size_t)(tw / SCAN_CHUNK) * D + ch;
             if (ch < D) a.chunk_states[i] = mine.x;
             if (ch + 1 < D) a.chunk_states[i + 1] = mine.y;
         }
-        if (!a.h && !(a.final_state && bd.ends)) continue;
         // the same tokens from that state
-        if (a.h && even && !(bd.starts | bd.ends) && tw >= sp.t0 && tw + NT <= sp.t1) {
-            uint8_t* to = static_cast<uint8_t*>(a.h) + ((size_t)tw * D + ch) * (a.out_bf16 ? 2 : 4);
-            const size_t row = (size_t)D * (a.out_bf16 ? 2 : 4);
-            if (a.out_bf16) {
+        if (plain) {
+            if (a.h && ch < D) {
+                const uint32_t row = (uint32_t)D * (a.out_bf16 ? 2 : 4);
+                uint8_t* const to = static_cast<uint8_t*>(a.h) + (size_t)tw * row + (size_t)ch * (a.out_bf16 ? 2 : 4);
+                if (a.out_bf16) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i, to += row) {
-                    mine = scan_step2(e[i], unpack2(lo[i]), mine, u[i]);
-                    if (ch < D) *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(mine.x, mine.y);
-                }
-            } else {
+                    for (int i = 0; i < NT; ++i) {
+                        const float2 h = __ffma2_rn(as[i], mine, hs[i]);
+                        *reinterpret_cast<uint32_t*>(to + (size_t)row * i) = pack_bf16x2(h.x, h.y);
+                    }
+                } else {
 #pragma unroll
-                for (int i = 0; i < NT; ++i, to += row) {
-                    mine = scan_step2(e[i], unpack2(lo[i]), mine, u[i]);
-                    if (ch < D) *reinterpret_cast<float2*>(to) = mine;
+                    for (int i = 0; i < NT; ++i)
+                        *reinterpret_cast<float2*>(to + (size_t)row * i) = __ffma2_rn(as[i], mine, hs[i]);
                 }
+            }
+            if (at.ends && a.final_state) {
+                const int n = at.seq_end(NT - 1);
+                if (n >= 0) store2(a.final_state, false, n, D, ch, __ffma2_rn(as[NT - 1], mine, hs[NT - 1]));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                mine = bd.starts >> i & 1 ? u[i] : scan_step2(e[i], unpack2(lo[i]), mine, u[i]);
-                if (a.h && tw + i >= sp.t0 && tw + i < sp.t1) store2(a.h, a.out_bf16, (size_t)(tw + i), D, ch, mine);
-                if (a.final_state && bd.ends >> i & 1) {
-                    const int64_t n = bd.seq_end(i);
-                    if (n >= 0) store2(a.final_state, false, (size_t)n, D, ch, mine);
+                const bool from_start = at.starts & ((2u << i) - 2u);
+                const float2 h = from_start ? hs[i] : __ffma2_rn(as[i], mine, hs[i]);
+                if (a.h && at.own >> i & 1) store2(a.h, a.out_bf16, (size_t)(tw + i), D, ch, h);
+                if (a.final_state && at.ends >> i & 1) {
+                    const int n = at.seq_end(i);
+                    if (n >= 0) store2(a.final_state, false, n, D, ch, h);
                 }
             }
         }
     }
     cp_wait<0>();
-    if (cluster > 1) {  // no CTA leaves while another may write to it
-        cluster_arrive();
-        cluster_wait();
-    }
+    if (failed && tma && lane == 0)  // loads still in flight
+        for (int s = n_steps < 2 ? 0 : n_steps - 2; s < n_steps; ++s) mbar_wait(full + (s & 1), (s >> 1) & 1, nullptr);
+    if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may write to it
     // sequences without tokens
     if (a.final_state && rank == 0) {
         for (int n = sp.n0 + warp; n < sp.n1; n += SC_WARPS) {
@@ -236,17 +312,17 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream) {
         const cudaError_t e = launch_scan_check(a, stream);
         if (e != cudaSuccess) return e;
     }
-    const void* in[] = {a.x, a.log_alpha, a.gate};
-    const int64_t ld[] = {a.ld_x, a.ld_l, a.ld_g};
-    const int width = scan_width(in, ld, a.gate ? 3 : 2, a.in_bf16);
-    cudaError_t e = cudaSuccess;
+    const void* in[] = {a.log_alpha, a.x, a.gate};
+    const int64_t ld[] = {a.ld_l, a.ld_x, a.ld_g};
+    ScanMaps maps;
+    int width = 0;
+    cudaError_t e = scan_maps(a, in, ld, a.gate ? 3 : 2, &maps, &width);
+    if (e != cudaSuccess) return e;
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
         if (a.in_bf16)
-            e = scan_launch<scan_fwd_kernel<true, G, W>>(ScanFwd<true, G, W>::SMEM, ScanFwd<true, G, W>::Geo::TILE, a,
-                                                         width, stream);
+            e = scan_launch<scan_fwd_kernel<true, G, W>>(ScanFwd<true, G>::smem, ScanGeo<true>::TILE, a, maps, width, stream);
         else
-            e = scan_launch<scan_fwd_kernel<false, G, W>>(ScanFwd<false, G, W>::SMEM, ScanFwd<false, G, W>::Geo::TILE, a,
-                                                          width, stream);
+            e = scan_launch<scan_fwd_kernel<false, G, W>>(ScanFwd<false, G>::smem, ScanGeo<false>::TILE, a, maps, width, stream);
     });
     return e;
 }

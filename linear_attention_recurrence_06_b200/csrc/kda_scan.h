@@ -1,11 +1,13 @@
 // kda_scan.h -- launch arguments of the element-wise gated scan (internal to libkda).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace kda {
 
 constexpr int SCAN_CHUNK = 64;  // tokens between two rows of chunk_states
+constexpr int64_t SCAN_MAX_TOKENS = (int64_t(1) << 31) - 65536;  // B * T: tokens are counted in 32 bits
 
 struct ScanArgs {
     const void *x, *log_alpha, *gate;
@@ -26,6 +28,10 @@ struct ScanArgs {
     const float* d_final;
     void *dx, *dl, *dg;
     float* d_init;
+};
+
+struct ScanMaps {
+    CUtensorMap m[4];  // log_alpha, x, gate, d_h
 };
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);

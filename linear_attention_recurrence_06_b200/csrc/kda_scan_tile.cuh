@@ -5,12 +5,14 @@
 // A CTA of 8 warps owns 64 channels (lane l: channels 2l and 2l + 1) and walks
 // tiles of 8 x NT tokens; warp w takes tokens NT w .. NT w + NT - 1 of a tile.  A
 // piece of the recurrence is affine in the state before it, h -> A h + B with
-// A = e^{sum l}, so a warp first runs its tokens from zero (A, B), the CTA folds the
-// warps' pieces over the carried state in order, and each warp then runs its
-// tokens again from the state it starts at, in registers.  The CTAs of a cluster
-// take neighbouring tiles and exchange their (A, B) through distributed shared
-// memory once per tile; every CTA folds all of them over its own copy of the
-// carried state, always from left to right: the result does not depend on timing.
+// A = e^{sum l}: a warp runs its tokens from zero, joins its piece (A, B) to those of
+// the warps before it and hands the result to the next warp; the last warp sends
+// the tile's piece to all CTAs of the cluster, which take neighbouring tiles.  Every
+// warp folds the pieces of all earlier tiles over a copy of its own of the carried
+// state and finishes its tokens in registers.  Pieces are always joined from left
+// to right: the result does not depend on timing.  Warps meet only at those
+// hand-overs (mbarriers); loads, too, are a warp's own, so that warps of
+// earlier tokens can be most of a step ahead of those that wait for them.
 // Why this split: the channels of one sequence alone (32 x 64 lanes for 4096) cannot
 // keep enough loads in flight, time has to be split; a cluster does that in one
 // pass over the data, without flags in global memory and without a second launch.
@@ -24,84 +26,101 @@ constexpr int SC_WARPS = 8, SC_THREADS = 256;
 constexpr int SC_CH = 64;           // channels of a CTA
 constexpr int SC_MAX_CLUSTER = 8;   // the portable limit
 
-template <bool BF16, int NT>
+template <bool BF16>
 struct ScanGeo {
     static constexpr int ES = BF16 ? 2 : 4;
+    static constexpr int NT = BF16 ? 16 : 8;      // tokens of a warp: 16 KB per tensor and tile
     static constexpr int TILE = SC_WARPS * NT;
     static constexpr int ROWB = SC_CH * ES;       // bytes of a tile's row
     static constexpr int TENS = TILE * ROWB;      // bytes of one tensor's tile
+    static_assert(SCAN_CHUNK % NT == 0 && TILE % SCAN_CHUNK == 0, "a chunk starts with a warp's tokens");
 };
 
 // ---- two channels at a time
 KDA_DEV float2 f2(float x, float y) { return make_float2(x, y); }
 KDA_DEV float2 f2(float x) { return make_float2(x, x); }
 
-// The tiled kernels keep a decay as e + lo: e = e^l as the hardware approximates it, lo what is missing to
-// 1 + (e^l - 1) with e^l - 1 from scan_decay's polynomial (0 where l <= -1/4, where e is good
-// enough).  A step is then two fused products for two channels at once, without a choice, and
-// keeps slow and fast decays as scan_step does.  lo is within a few 2^-24 and its own error
-// does not matter, so two of them wait in one register as bf16 for the second run.
+// The tiled kernels keep a decay as e + lo: e = e^l as the hardware approximates it, lo what is missing
+// to 1 - m, m = 1 - e^l by its Taylor polynomial where l > -1/4 (and 1 - e, so that lo = 0, elsewhere).  A
+// step is then two fused products for two channels at once, without a choice, and keeps slow
+// and fast decays as scan_step does.  `d` = -l >= 0.
 struct ScanDecay2 {
-    float2 e, lo, em;  // em = e^l - 1
+    float2 e, lo, m;
 };
-KDA_DEV ScanDecay2 scan_decay2(float2 l) {
+KDA_DEV ScanDecay2 scan_decay2(float2 d) {
     ScanDecay2 r;
-    float2 t = __ffma2_rn(l, f2(1.f / 720.f), f2(1.f / 120.f));
-    t = __ffma2_rn(t, l, f2(1.f / 24.f));
-    t = __ffma2_rn(t, l, f2(1.f / 6.f));
-    t = __ffma2_rn(t, l, f2(0.5f));
-    const float2 slow = __ffma2_rn(__fmul2_rn(t, l), l, l);
-    const float2 x = __fmul2_rn(l, f2(LOG2E));
+    float2 t = __ffma2_rn(d, f2(-1.f / 720.f), f2(1.f / 120.f));
+    t = __ffma2_rn(t, d, f2(-1.f / 24.f));
+    t = __ffma2_rn(t, d, f2(1.f / 6.f));
+    t = __ffma2_rn(t, d, f2(-0.5f));
+    const float2 slow = __ffma2_rn(__fmul2_rn(t, d), d, d);
+    const float2 x = __fmul2_rn(d, f2(-LOG2E));
     r.e = f2(ex2_ftz(x.x), ex2_ftz(x.y));
-    const float2 e1 = __fadd2_rn(r.e, f2(-1.f));
-    r.em = f2(l.x > SCAN_SLOW ? slow.x : e1.x, l.y > SCAN_SLOW ? slow.y : e1.y);
-    r.lo = __ffma2_rn(e1, f2(-1.f), r.em);
+    const float2 m1 = __ffma2_rn(r.e, f2(-1.f), f2(1.f));
+    r.m = f2(d.x < -SCAN_SLOW ? slow.x : m1.x, d.y < -SCAN_SLOW ? slow.y : m1.y);
+    r.lo = __ffma2_rn(r.m, f2(-1.f), m1);
     return r;
 }
 KDA_DEV float2 scan_step2(float2 e, float2 lo, float2 h, float2 u) { return __ffma2_rn(lo, h, __ffma2_rn(e, h, u)); }
-KDA_DEV float2 unpack2(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+// -l of two channels: max(-log_alpha, 0), NaN kept
+KDA_DEV float2 scan_depth2(float2 log_alpha) {
+    float2 r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(-log_alpha.x), "f"(0.f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(-log_alpha.y), "f"(0.f));
+    return r;
+}
 
-// w s of two channels (scan_term's), and s
+// w s of two channels.  With both factors w s = sqrt(n) / q = n rsqrt(n q^2), n = 1 - a^2, q = 1 + e^-gate:
+// one special function less (the forward spends three per value then; at four they alone
+// take as long as the memory).  q^2 overflows for a gate below -44: s = 1e-19 counts as 0 there.
 template <bool GATE, bool NORM>
-KDA_DEV float2 scan_weight2(float2 em, float2 g, float2* s) {
-    float2 ws = f2(1.f);
+KDA_DEV float2 scan_weight2(float2 m, float2 g) {
+    float2 q = f2(1.f);
     if (GATE) {
         const float2 x = __fmul2_rn(g, f2(-LOG2E));
-        const float2 d = __fadd2_rn(f2(ex2_ftz(x.x), ex2_ftz(x.y)), f2(1.f));
-        ws = f2(rcp_ftz(d.x), rcp_ftz(d.y));
-        *s = ws;
+        q = __fadd2_rn(f2(ex2_ftz(x.x), ex2_ftz(x.y)), f2(1.f));
     }
-    if (NORM) {
-        const float2 n = __ffma2_rn(em, __fmul2_rn(em, f2(-1.f)), __fmul2_rn(em, f2(-2.f)));  // 1 - a^2
-        const float2 w = __fmul2_rn(n, f2(rsqrt_ftz(fmaxf(n.x, SCAN_TINY)), rsqrt_ftz(fmaxf(n.y, SCAN_TINY))));
-        ws = GATE ? __fmul2_rn(ws, w) : w;
-    }
-    return ws;
+    if (!NORM) return GATE ? f2(rcp_ftz(q.x), rcp_ftz(q.y)) : f2(1.f);
+    const float2 n = __fmul2_rn(m, __ffma2_rn(m, f2(-1.f), f2(2.f)));
+    float2 r = __fadd2_rn(n, f2(SCAN_TINY));
+    if (GATE) r = __fmul2_rn(__fmul2_rn(r, q), q);
+    return __fmul2_rn(n, f2(rsqrt_ftz(r.x), rsqrt_ftz(r.y)));
 }
 
-// A piece is kept as (A, B) of both channels in a float4 {A0, A1, B0, B1}, A in scan_decay's
-// form (hundreds of slow pieces in a row would show the rounding of A itself), SCAN_CUT for
-// a piece in which a sequence starts: nothing of the state before it gets through.
-constexpr float SCAN_CUT = -2.f;
-KDA_DEV float scan_fold(float A, float B, float h) { return A < -1.f ? B : scan_step(A, h, B); }
-KDA_DEV float2 scan_fold2(float4 ab, float2 h) { return f2(scan_fold(ab.x, ab.z, h.x), scan_fold(ab.y, ab.w, h.y)); }
-// A of two pieces in a row
-KDA_DEV float scan_join_a(float a, float b) {
-    if (a < -1.f || b < -1.f) return SCAN_CUT;
-    if (scan_slow(a) && scan_slow(b)) return __uint_as_float(__float_as_uint(fmaf(a, b, a + b)) | 0x80000000u);
-    return scan_a(a) * scan_a(b);
+// A piece of the recurrence, h -> A h + B, of both channels in a float4 {A0, A1, B0, B1}, A in scan_decay's
+// form (hundreds of slow pieces in a row would show the rounding of A itself), SC_CUT in
+// both for a piece in which a sequence starts: nothing of the state before it gets through.
+constexpr float SC_CUT = -2.f;
+KDA_DEV float2 scan_step2(float2 p, float2 h, float2 u) {
+    const float2 t = __ffma2_rn(p, h, u);
+    return __fadd2_rn(t, f2(__uint_as_float(__float_as_uint(h.x) & (uint32_t)(__float_as_int(p.x) >> 31)),
+                            __uint_as_float(__float_as_uint(h.y) & (uint32_t)(__float_as_int(p.y) >> 31))));
 }
-// the piece `ab` behind the piece `acc`, as one
-KDA_DEV float4 scan_join(float4 acc, float4 ab) {
-    return make_float4(scan_join_a(acc.x, ab.x), scan_join_a(acc.y, ab.y), scan_fold(ab.x, ab.z, acc.z),
-                       scan_fold(ab.y, ab.w, acc.w));
+KDA_DEV float4 scan_piece(bool cut, float2 depth, float2 b) {
+    const ScanDecay2 d = scan_decay2(depth);
+    const float2 p = f2(depth.x < -SCAN_SLOW ? -d.m.x : d.e.x, depth.y < -SCAN_SLOW ? -d.m.y : d.e.y);
+    return make_float4(cut ? SC_CUT : p.x, cut ? SC_CUT : p.y, b.x, b.y);
+}
+KDA_DEV float2 scan_fold2(float4 v, float2 h) { return scan_step2(f2(v.x, v.y), h, f2(v.z, v.w)); }
+KDA_DEV float2 scan_fold2(float4 v, float2 h, bool cut) { return cut ? f2(v.z, v.w) : scan_fold2(v, h); }
+// A of two pieces in a row, none of them cut
+KDA_DEV float scan_join_a(float a, float b) {
+    return scan_slow(a) && scan_slow(b) ? __uint_as_float(__float_as_uint(fmaf(a, b, a + b)) | 0x80000000u)
+                                        : scan_a(a) * scan_a(b);
+}
+KDA_DEV bool scan_is_cut(float4 v) { return v.x < -1.f; }
+// the piece v behind the piece all
+KDA_DEV float4 scan_join2(float4 all, float4 v) {
+    const bool cut = scan_is_cut(v);
+    const float2 b = scan_fold2(v, f2(all.z, all.w), cut);
+    if (cut || scan_is_cut(all)) return make_float4(SC_CUT, SC_CUT, b.x, b.y);
+    return make_float4(scan_join_a(all.x, v.x), scan_join_a(all.y, v.y), b.x, b.y);
 }
 
 // ---- loads
-// 16, 8 or 4 bytes, of which `n` are read and the rest zero
-KDA_DEV void cp_async16_zfill(uint32_t dst, const void* src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
+// A warp's NT rows of one tensor come by TMA where its rows are 16-byte aligned (zeros behind the
+// last row and channel), else by asynchronous copies of 4 bytes, or by plain loads of odd
+// rows of 2-byte values; tokens outside [t0, t1) and channels from D on become zeros.
 KDA_DEV void cp_async4_zfill(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -109,64 +128,30 @@ KDA_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); 
 template <int N>
 KDA_DEV void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// This warp's NT rows of one tensor's tile, token tw the first of them, into `dst` (the
-// tile's start in shared memory): tokens outside [t0, t1) and channels from D on become
-// zeros, which leave a state as it is.  `width`: bytes of a copy that the tensor's address
-// and stride allow (16, 4, or 2: plain loads).
-template <bool BF16, int NT>
-KDA_DEV void load_rows(uint8_t* dst, const void* base, int64_t ld, int64_t tw, int64_t t0, int64_t t1, int ch0, int D,
-                       int width, int warp, int lane) {
-    using Geo = ScanGeo<BF16, NT>;
+template <bool BF16>
+__device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t ld, int tw, int t0, int t1, int ch0, int D,
+                                       int width, int lane) {
+    using Geo = ScanGeo<BF16>;
     constexpr int ES = Geo::ES;
-    uint8_t* const rows = dst + warp * NT * Geo::ROWB;
+    uint8_t* const rows = dst;
     const uint8_t* const src = static_cast<const uint8_t*>(base);
-    const bool whole = tw >= t0 && tw + NT <= t1;
-    if (width == 16) {
-        constexpr int PR = Geo::ROWB / 16;  // pieces of a row
-        constexpr int RPI = 32 / PR;        // rows of a warp-wide copy
-        const int col = lane % PR, row0 = lane / PR, ch = ch0 + col * (16 / ES);
-        const int left = (D - ch) * ES;
-        const int n = left < 0 ? 0 : (left > 16 ? 16 : left);
-        const uint32_t to = smem_u32(rows) + row0 * Geo::ROWB + col * 16;
-        const int64_t step = ld * (RPI * ES);
-        const uint8_t* from = src + (tw + row0) * ld * ES + (int64_t)ch * ES;
-        if (whole) {
-            if (n == 0) from = src;
-            const int64_t st = n == 0 ? 0 : step;
+    for (int i = 0; i < Geo::NT; ++i) {
+        const int t = tw + i;
+        const bool row_in = t >= t0 && t < t1;
+        if (!BF16 || width == 4) {
 #pragma unroll
-            for (int i = 0; i < NT / RPI; ++i, from += st) cp_async16_zfill(to + i * RPI * Geo::ROWB, from, n);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NT / RPI; ++i, from += step) {
-                const int64_t t = tw + row0 + i * RPI;
-                const bool in = n > 0 && t >= t0 && t < t1;
-                cp_async16_zfill(to + i * RPI * Geo::ROWB, in ? from : src, in ? n : 0);
-            }
-        }
-    } else if (width == 4) {
-        constexpr int PL = Geo::ROWB / 128;  // 4-byte pieces of a row per lane
-#pragma unroll 4
-        for (int i = 0; i < NT; ++i) {
-            const int64_t t = tw + i;
-            const bool row_in = t >= t0 && t < t1;
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
+            for (int k = 0; k < Geo::ROWB / 128; ++k) {
                 const int ch = ch0 + (lane + 32 * k) * (4 / ES);
                 const int left = (D - ch) * ES, n = left < 0 ? 0 : (left > 4 ? 4 : left);
                 const bool in = row_in && n > 0;
                 cp_async4_zfill(smem_u32(rows + i * Geo::ROWB + (lane + 32 * k) * 4),
                                 in ? src + ((size_t)t * ld + ch) * ES : src, in ? n : 0);
             }
-        }
-    } else {
-        const uint16_t* const s = reinterpret_cast<const uint16_t*>(src);
-        const int ch = ch0 + 2 * lane;
-#pragma unroll 8
-        for (int i = 0; i < NT; ++i) {
-            const int64_t t = tw + i;
-            const bool in = t >= t0 && t < t1;
-            const uint32_t lo = in && ch < D ? s[(size_t)t * ld + ch] : 0u;
-            const uint32_t hi = in && ch + 1 < D ? s[(size_t)t * ld + ch + 1] : 0u;
+        } else {
+            const uint16_t* const s = reinterpret_cast<const uint16_t*>(src) + (size_t)(row_in ? t : t0) * ld;
+            const int ch = ch0 + 2 * lane;
+            const uint32_t lo = row_in && ch < D ? s[ch] : 0u;
+            const uint32_t hi = row_in && ch + 1 < D ? s[ch + 1] : 0u;
             *reinterpret_cast<uint32_t*>(rows + i * Geo::ROWB + lane * 4) = lo | hi << 16;
         }
     }
@@ -184,7 +169,7 @@ KDA_DEV float2 tile_at(const uint8_t* tile, int row, int lane) {
 }
 
 // Two channels of a row of an output [tokens, D].
-KDA_DEV void store2(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
+__device__ __noinline__ void store2(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
     const size_t i = row * D + ch;
     if (ch + 1 < D && (D & 1) == 0) {
         if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + i) = pack_bf16x2(v.x, v.y);
@@ -207,7 +192,7 @@ KDA_DEV float2 load2(const float* base, size_t row, int D, int ch) {
 
 // ---- sequences
 // First m in [lo, hi) with cu[m] >= v (hi if there is none); all lanes of a warp.
-KDA_DEV int warp_lower_bound(const int32_t* __restrict__ cu, int lo, int hi, int64_t v, int lane) {
+KDA_DEV int warp_lower_bound(const int32_t* __restrict__ cu, int lo, int hi, int v, int lane) {
     while (lo < hi) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + lane * step;
@@ -221,29 +206,28 @@ KDA_DEV int warp_lower_bound(const int32_t* __restrict__ cu, int lo, int hi, int
 }
 
 // The part of the packed tokens that split `s` of `S` walks: whole sequences n0 .. n1 - 1,
-// tokens [t0, t1).
+// tokens [t0, t1).  (Tokens are counted in 32 bits; offsets of elements in 64.)
 struct ScanSpan {
-    int n0, n1;
-    int64_t t0, t1;
+    int n0, n1, t0, t1;
 };
 KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int lane) {
     ScanSpan r;
     if (!a.cu) {
-        r.n0 = (int)((int64_t)a.B * s / S);
-        r.n1 = (int)((int64_t)a.B * (s + 1) / S);
-        r.t0 = (int64_t)r.n0 * a.T;
-        r.t1 = (int64_t)r.n1 * a.T;
+        r.n0 = S == 1 ? 0 : (int)((int64_t)a.B * s / S);
+        r.n1 = S == 1 ? a.B : (int)((int64_t)a.B * (s + 1) / S);
+        r.t0 = r.n0 * (int)a.T;
+        r.t1 = r.n1 * (int)a.T;
         return r;
     }
-    int64_t end = a.cu[a.n_seqs];
-    end = end < 0 ? 0 : (end > a.T ? a.T : end);
+    int end = a.cu[a.n_seqs];
+    end = end < 0 ? 0 : (end > (int)a.T ? (int)a.T : end);
     r.n0 = 0, r.n1 = a.n_seqs, r.t0 = 0, r.t1 = end;
     if (s > 0) {
-        r.n0 = warp_lower_bound(a.cu, 0, a.n_seqs, end * s / S, lane);
+        r.n0 = warp_lower_bound(a.cu, 0, a.n_seqs, (int)((int64_t)end * s / S), lane);
         r.t0 = r.n0 < a.n_seqs ? a.cu[r.n0] : end;
     }
     if (s + 1 < S) {
-        r.n1 = warp_lower_bound(a.cu, 0, a.n_seqs, end * (s + 1) / S, lane);
+        r.n1 = warp_lower_bound(a.cu, 0, a.n_seqs, (int)((int64_t)end * (s + 1) / S), lane);
         r.t1 = r.n1 < a.n_seqs ? a.cu[r.n1] : end;
     }
     if (r.t0 < 0) r.t0 = 0;
@@ -253,76 +237,120 @@ KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int lane) {
 }
 
 // Where sequences meet among a warp's NT tokens: bit j of `starts` / `ends`: token tw + j is the
-// first / last of its sequence; whose numbers are seq_start(j) and seq_end(j) (which a
-// cu_seqlens that starts behind 0 can make -1).
-template <int NT>
-struct ScanBounds {
-    uint32_t starts, ends;
-    int64_t n;      // equal lengths: sequence of token tw, and tw's place in it
-    uint32_t r, T;
-    int* tab;       // packed: [2][NT] of this warp: last m with cu[m] = tw + j, first with cu[m] = tw + j + 1
-    KDA_DEV int64_t seq_start(int j) const { return tab ? tab[j] : n + (r + j) / T; }
-    KDA_DEV int64_t seq_end(int j) const { return tab ? tab[NT + j] - 1 : n + (r + j) / T; }
+// first / last of its sequence, whose number is seq_start(j) / seq_end(j) (-1 can come of a
+// cu_seqlens that begins behind 0); bit j of `own`: the token is one of this split's.  Until
+// step `calm` there is nothing more to see, and scan_look() need not be called.
+struct ScanSeen {
+    uint32_t starts, ends, own;
+    int calm;
+    int lane_start, lane_end;  // lane j: the sequences that start at and end with token tw + j
+    KDA_DEV int seq_start(int j) const { return __shfl_sync(0xffffffffu, lane_start, j); }
+    KDA_DEV int seq_end(int j) const { return __shfl_sync(0xffffffffu, lane_end, j); }
 };
 
+// For step s, whose tokens begin at tw; those of the next steps at tw + by, tw + 2 by, ...  `tab`: 2 NT
+// ints of shared memory of this warp, used before the return.  Returns {starts | ends << 16,
+// own | steps until the next look << 16, lane_start, lane_end}, the first two the same on all lanes.
+// Rarely called: kept out of the loop, and its arguments and result in registers.
 template <int NT>
-KDA_DEV ScanBounds<NT> scan_bounds(const ScanArgs& a, const ScanSpan& sp, int64_t tw, int* ptr, int* tab, int lane) {
-    ScanBounds<NT> b;
-    uint32_t meet = 0;  // bit j: a sequence starts at token tw + j, j = 0 .. NT
-    if (!a.cu) {
-        b.tab = nullptr;
-        if (a.T > 0) {
-            b.n = tw / a.T;
-            const int64_t r = tw - b.n * a.T, left = a.T - r;
-            if (a.T >> 31) {  // a length past 32 bits: at most one meeting point, `left` tokens ahead
-                b.r = 0;
-                b.T = left > NT ? NT + 1 : (uint32_t)left;
-                meet = (r == 0 ? 1u : 0u) | (left <= NT ? 1u << (int)left : 0u);
-            } else {
-                b.r = (uint32_t)r;
-                b.T = (uint32_t)a.T;
-                meet = __ballot_sync(0xffffffffu, lane <= NT && (b.r + lane) % b.T == 0);
-            }
-        }
+__device__ __noinline__ uint4 scan_look(const int32_t* __restrict__ cu, int n_seqs, int T, int t0, int t1, int tw,
+                                        int by, int* tab) {
+    constexpr uint32_t ALL = (1u << NT) - 1u;
+    const int lane = threadIdx.x & 31;
+    uint32_t own = ALL;
+    if (tw < t0) own = t0 - tw >= NT ? 0u : own & ~((1u << (t0 - tw)) - 1u);
+    if (tw + NT > t1) own = tw >= t1 ? 0u : own & ((1u << (t1 - tw)) - 1u);
+    if (own == 0) return make_uint4(0u, 1u << 16, 0u, 0u);
+    int prev, next;  // the last meeting point before tw, the first at or behind it
+    int m = 0;
+    const int N1 = n_seqs + 1;
+    if (cu) {
+        m = warp_lower_bound(cu, 0, N1, tw, lane);
+        next = m < N1 ? cu[m] : INT32_MAX;
+        prev = m > 0 ? cu[m - 1] : -1;
     } else {
-        b.tab = tab;
-        const int N1 = a.n_seqs + 1;
-        int m = *ptr;
-        const int v0 = m + lane < N1 ? a.cu[m + lane] : INT32_MAX;
-        const int k = __popc(__ballot_sync(0xffffffffu, v0 < tw));
-        m = k < 32 ? m + k : warp_lower_bound(a.cu, m + 32 < N1 ? m + 32 : N1, N1, tw, lane);
-        *ptr = m;
-        __syncwarp();
+        const int r = tw % T;
+        next = r == 0 ? tw : (T > INT32_MAX - tw + r ? INT32_MAX : tw - r + T);
+        prev = r == 0 ? tw - T : tw - r;
+    }
+    if (next > tw + NT) {
+        if (own != ALL) return make_uint4(0u, own | 1u << 16, 0u, 0u);
+        // nothing to look at while tw + NT < next and tw + NT <= t1 (forwards), tw > prev and
+        // tw >= t0 (backwards)
+        const int room = by > 0 ? (next < t1 + 1 ? next : t1 + 1) - NT - tw : tw - (prev > t0 - 1 ? prev : t0 - 1);
+        const int step = by > 0 ? by : -by, steps = (room - 1) / step + 1;
+        return make_uint4(0u, own | (uint32_t)(steps < 1 ? 1 : (steps > 65535 ? 65535 : steps)) << 16, 0u, 0u);
+    }
+    uint32_t meet = 0;  // bit j: a sequence starts at tw + j, j = 0 .. NT
+    int lane_start, lane_end;
+    __syncwarp();
+    if (cu) {
         int before = -1;  // the value of the entry before the window
-        while (m < N1) {
-            const int v = m + lane < N1 ? a.cu[m + lane] : INT32_MAX;
+        for (int k = m; k < N1; k += 32) {
+            const int v = k + lane < N1 ? cu[k + lane] : INT32_MAX;
             const int up = __shfl_up_sync(0xffffffffu, v, 1), down = __shfl_down_sync(0xffffffffu, v, 1);
             const bool in = v >= tw && v <= tw + NT;
-            const int j = in ? (int)(v - tw) : 0;
-            if (in && j < NT && (lane == 31 || down != v)) tab[j] = m + lane;
-            if (in && j > 0 && (lane == 0 ? before != v : up != v)) tab[NT + j - 1] = m + lane;
+            const int j = in ? v - tw : 0;
+            if (in && j < NT && (lane == 31 || down != v)) tab[j] = k + lane;  // the last entry of a value
+            if (in && j > 0 && (lane == 0 ? before != v : up != v)) tab[NT + j - 1] = k + lane - 1;  // the first
             meet |= __reduce_or_sync(0xffffffffu, in ? 1u << j : 0u);
             before = __shfl_sync(0xffffffffu, v, 31);
             if (__ballot_sync(0xffffffffu, in) != 0xffffffffu) break;
-            m += 32;
             __syncwarp();
         }
         __syncwarp();
+        lane_start = lane < NT ? tab[lane] : 0;
+        lane_end = lane < NT ? tab[NT + lane] : 0;
+        __syncwarp();
+    } else {
+        const int t = tw + lane, n = t / T;
+        lane_start = n;
+        lane_end = (t + 1) / T - 1;
+        meet = __ballot_sync(0xffffffffu, lane <= NT && n * T == t);
     }
-    // only tokens of [t0, t1)
-    uint32_t own = NT < 32 ? (1u << NT) - 1u : 0xffffffffu;
-    if (tw < sp.t0) own = sp.t0 - tw >= NT ? 0u : own & ~((1u << (int)(sp.t0 - tw)) - 1u);
-    if (tw + NT > sp.t1) own = tw >= sp.t1 ? 0u : own & ((1u << (int)(sp.t1 - tw)) - 1u);
-    b.starts = meet & own;
-    b.ends = (meet >> 1) & own;
-    return b;
+    return make_uint4((meet & own) | ((meet >> 1) & own) << 16, own | 1u << 16, (uint32_t)lane_start, (uint32_t)lane_end);
+}
+// The same as ScanSeen; `calm`: the step to look again.
+template <int NT>
+KDA_DEV ScanSeen scan_see(const ScanArgs& a, const ScanSpan& sp, int s, int tw, int by, int* tab) {
+    const uint4 r = scan_look<NT>(a.cu, a.n_seqs, (int)a.T, sp.t0, sp.t1, tw, by, tab);
+    ScanSeen v;
+    v.starts = r.x & 0xffffu;
+    v.ends = r.x >> 16;
+    v.own = r.y & 0xffffu;
+    v.lane_start = (int)r.z;
+    v.lane_end = (int)r.w;
+    v.calm = s + (int)(r.y >> 16);  // the same on all lanes, like the masks
+    return v;
 }
 
 // ---- clusters
 KDA_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 KDA_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-KDA_DEV void st_cluster(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// Waits like mbar_wait, for what other CTAs of the cluster have written.
+KDA_DEV bool mbar_wait_peers(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+            : "memory");
+        if (ok) return true;
+        if (t0 == 0) t0 = globaltimer_ns();
+        else if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            if (status) atomicOr(status, DEV_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+// 16 bytes into a CTA's shared memory, counted on its barrier
+KDA_DEV void st_async16(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
 }
 
