@@ -386,7 +386,7 @@ KDA_API kda_status kda_gate_norm(const void* o, const void* gate, const float* n
 #define KDA_STATUS_BYTES 256u
 
 /* Tokens between two rows of chunk_states below. */
-#define KDA_SCAN_CHUNK 64
+#define KDA_SCAN_CHUNK 8
 
 /*
  * kda_scan_fwd -- h for every token and the last state of every sequence.

@@ -37,7 +37,7 @@ LIB_PATH = os.path.join(_PKG, "libkda.so")
 KDA_OK = 0
 KDA_F32, KDA_BF16 = 0, 1
 HEAD_DIM = 128
-SCAN_CHUNK = 64  # tokens between two rows of scan_fwd's chunk_states
+SCAN_CHUNK = 8  # tokens between two rows of scan_fwd's chunk_states
 
 _STATUS_NAMES = {
     0: "KDA_OK", -1: "KDA_ERR_INVALID_ARG", -2: "KDA_ERR_UNSUPPORTED", -3: "KDA_ERR_MISALIGNED",

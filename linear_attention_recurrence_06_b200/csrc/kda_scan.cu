@@ -10,7 +10,7 @@
 
 namespace kda {
 
-bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, bool bf16) {
+bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool bf16) {
     static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encoder{nullptr};
     PFN_cuTensorMapEncodeTiled_v12000 enc = encoder.load(std::memory_order_relaxed);
     if (!enc) {
@@ -24,7 +24,7 @@ bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
     }
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
-    const cuuint32_t box[2] = {SC_CH, (cuuint32_t)(bf16 ? ScanGeo<true>::NT : ScanGeo<false>::NT)}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {SC_CH, (cuuint32_t)box_rows}, one[2] = {1, 1};
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
                dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -38,9 +38,9 @@ namespace {
 // inside a token's output; what is carried on goes by the sum of the log-decays.)
 template <bool BF16, bool GATE>
 struct ScanFwd {
-    using Geo = ScanGeo<BF16>;
+    static constexpr int NT = BF16 ? 16 : 8;                                 // tokens of a warp
     static constexpr int N_IN = GATE ? 3 : 2;
-    static constexpr int ROWS = Geo::NT * Geo::ROWB;                         // a warp's rows of one tensor
+    static constexpr int ROWS = NT * ScanGeo<BF16>::ROWB;                         // a warp's rows of one tensor
     static constexpr int STAGE = N_IN * ROWS;                                // [warps][2] stages
     static constexpr int OFF_AB = SC_WARPS * 2 * STAGE;                      // [2][warps][32] pieces up to a warp
     static constexpr int OFF_BAR = OFF_AB + 2 * SC_WARPS * 512;              // full[warps][2], given[warps][2], sent[4][cluster]
@@ -53,8 +53,7 @@ template <bool BF16, bool GATE, bool NORM>
 __global__ void __launch_bounds__(SC_THREADS, 2)
 scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
     using K = ScanFwd<BF16, GATE>;
-    using Geo = ScanGeo<BF16>;
-    constexpr int NT = Geo::NT, TILE = Geo::TILE;
+    constexpr int NT = K::NT, TILE = SC_WARPS * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % cluster, ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
@@ -92,9 +91,9 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             }
         } else {
             if (s < n_steps) {
-                load_rows<BF16>(st, a.log_alpha, a.ld_l, t, sp.t0, sp.t1, ch0, D, width, lane);
-                load_rows<BF16>(st + K::ROWS, a.x, a.ld_x, t, sp.t0, sp.t1, ch0, D, width, lane);
-                if (GATE) load_rows<BF16>(st + 2 * K::ROWS, a.gate, a.ld_g, t, sp.t0, sp.t1, ch0, D, width, lane);
+                load_rows<BF16, NT>(st, a.log_alpha, a.ld_l, t, sp.t0, sp.t1, ch0, D, width, lane);
+                load_rows<BF16, NT>(st + K::ROWS, a.x, a.ld_x, t, sp.t0, sp.t1, ch0, D, width, lane);
+                if (GATE) load_rows<BF16, NT>(st + 2 * K::ROWS, a.gate, a.ld_g, t, sp.t0, sp.t1, ch0, D, width, lane);
             }
             cp_commit();
         }
@@ -202,10 +201,14 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         float2 mine = warp > 0 ? scan_fold2(before, carry, scan_is_cut(before)) : carry;
         if (at.starts & 1) mine = h0;
 
-        if (warp % (SCAN_CHUNK / NT) == 0 && a.chunk_states && tw >= sp.t0 && tw < sp.t1) {
-            const size_t i = (size_t)(tw / SCAN_CHUNK) * D + ch;
-            if (ch < D) a.chunk_states[i] = mine.x;
-            if (ch + 1 < D) a.chunk_states[i + 1] = mine.y;
+        if (a.chunk_states) {
+#pragma unroll
+            for (int i = 0; i < NT; i += SCAN_CHUNK) {  // the state before token i
+                const bool own = at.own >> i & 1, from_start = at.starts & ((1u << i) - 2u) & ((1u << i) - 1u);
+                float2 h = mine;
+                if (i > 0) h = from_start ? hs[i - 1] : __ffma2_rn(as[i - 1], mine, hs[i - 1]);
+                if (own) store2(a.chunk_states, false, (tw + i) / SCAN_CHUNK, D, ch, h);
+            }
         }
         // the same tokens from that state
         if (plain) {
@@ -289,17 +292,6 @@ scan_decode_kernel(float* state, const void* x, const void* log_alpha, const voi
 
 }  // namespace
 
-#define KDA_SCAN_GN(GATE, NORM, ...)                                     \
-    do {                                                                 \
-        if (GATE) {                                                      \
-            if (NORM) { constexpr bool G = true, W = true; __VA_ARGS__; }       \
-            else      { constexpr bool G = true, W = false; __VA_ARGS__; }      \
-        } else {                                                         \
-            if (NORM) { constexpr bool G = false, W = true; __VA_ARGS__; }      \
-            else      { constexpr bool G = false, W = false; __VA_ARGS__; }     \
-        }                                                                \
-    } while (0)
-
 cudaError_t launch_scan_check(const ScanArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream);
     if (e != cudaSuccess || !a.cu) return e;
@@ -316,13 +308,15 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream) {
     const int64_t ld[] = {a.ld_l, a.ld_x, a.ld_g};
     ScanMaps maps;
     int width = 0;
-    cudaError_t e = scan_maps(a, in, ld, a.gate ? 3 : 2, &maps, &width);
+    cudaError_t e = scan_maps(a, in, ld, a.gate ? 3 : 2, a.in_bf16 ? ScanFwd<true, true>::NT : ScanFwd<false, true>::NT, &maps, &width);
     if (e != cudaSuccess) return e;
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
         if (a.in_bf16)
-            e = scan_launch<scan_fwd_kernel<true, G, W>>(ScanFwd<true, G>::smem, ScanGeo<true>::TILE, a, maps, width, stream);
+            e = scan_launch<scan_fwd_kernel<true, G, W>>(ScanFwd<true, G>::smem, SC_WARPS * ScanFwd<true, G>::NT, a, maps,
+                                                         width, stream);
         else
-            e = scan_launch<scan_fwd_kernel<false, G, W>>(ScanFwd<false, G>::smem, ScanGeo<false>::TILE, a, maps, width, stream);
+            e = scan_launch<scan_fwd_kernel<false, G, W>>(ScanFwd<false, G>::smem, SC_WARPS * ScanFwd<false, G>::NT, a,
+                                                          maps, width, stream);
     });
     return e;
 }

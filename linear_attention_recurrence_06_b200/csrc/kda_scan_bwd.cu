@@ -1,55 +1,286 @@
 // kda_scan_bwd.cu -- gradients of the element-wise gated scan (include/kda.h,
-// kda_scan_bwd).  The states inside a chunk of 64 tokens are computed again from
-// the state before it; then the gradient G_t = dh_t + a_{t+1} G_{t+1} walks back.
-#include "kda_scan.h"
-#include "kda_scan.cuh"
+// kda_scan_bwd): G_t = dh_t + a_{t+1} G_{t+1} walks back over the tokens, c_t = a_t G_t goes on to the
+// token before, and each gradient is G times a factor of its token:
+//     dx = G (w s),   dgate = G (u (1 - s)),   dlog_alpha = G (a h_{t-1} - a^2 u / (1 - a^2))
+// (a^2 s x / w = a^2 u / w^2).  Split as the forward (kda_scan_tile.cuh), with time reversed: warp 0 has a
+// tile's last tokens, CTA 0 of a cluster the last tile.  A warp first runs its 8 tokens forwards
+// from the state before them, which the forward keeps for every 8 tokens (half a byte per value;
+// without it the warps' states would have to be handed on as well, before they could begin to
+// walk back), for the factors; then back from zero.  HBM-bound: 14.5 bytes per value in bf16.
+#include <type_traits>
+
+#include "kda_scan_launch.h"
 
 namespace kda {
 
 namespace {
 
-template <bool GATE, bool NORM>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(ScanArgs a) {
-    const int ch = blockIdx.x * 128 + threadIdx.x, n = blockIdx.y;
-    if (ch >= a.D) return;
-    int64_t first, end;
-    scan_range(a.cu, n, a.T, &first, &end);
-    const float h0 = a.init ? a.init[(size_t)n * a.D + ch] : 0.f;
-    float c = a.d_final ? a.d_final[(size_t)n * a.D + ch] : 0.f;  // a_{t+1} G_{t+1}
-    auto in = [&](const void* p, int64_t t, int64_t ld) {
-        const size_t i = (size_t)t * ld + ch;
-        return a.in_bf16 ? ld_in<true>(p, i) : ld_in<false>(p, i);
-    };
-    auto out = [&](void* p, int64_t t, float v) {
-        const size_t i = (size_t)t * a.D + ch;
-        if (a.out_bf16) st_out<true>(p, i, v);
-        else st_out<false>(p, i, v);
-    };
-    float hp[SCAN_CHUNK];  // the state before each token of the chunk
-    for (int64_t ce = end; ce > first;) {
-        int64_t cs = (ce - 1) / SCAN_CHUNK * SCAN_CHUNK;
-        float h = cs > first ? a.chunk_states[(size_t)(cs / SCAN_CHUNK) * a.D + ch] : h0;
-        if (cs < first) cs = first;
-        for (int64_t t = cs; t < ce; ++t) {
-            hp[t - cs] = h;
-            const ScanTerm r = scan_term<GATE, NORM>(in(a.x, t, a.ld_x), in(a.log_alpha, t, a.ld_l),
-                                                     GATE ? in(a.gate, t, a.ld_g) : 0.f);
-            h = scan_step(r.p, h, r.u);
-        }
-        for (int64_t t = ce - 1; t >= cs; --t) {
-            const float l = in(a.log_alpha, t, a.ld_l);
-            const ScanTerm r = scan_term<GATE, NORM>(in(a.x, t, a.ld_x), l, GATE ? in(a.gate, t, a.ld_g) : 0.f);
-            const float G = in(a.d_h, t, a.ld_dh) + c;
-            out(a.dx, t, G * r.ws);
-            float dl = scan_a(r.p) * hp[t - cs];
-            if (NORM) dl += scan_du_dl(r);
-            out(a.dl, t, l > 0.f ? 0.f : G * dl);
-            if (GATE) out(a.dg, t, G * r.u * (1.f - r.s));
-            c = scan_step(r.p, G, 0.f);
-        }
-        ce = cs;
+template <bool BF16, bool GATE>
+struct ScanBwd {
+    static constexpr int NT = SCAN_CHUNK;                                    // tokens of a warp
+    static constexpr int N_IN = GATE ? 4 : 3;
+    static constexpr int ROWS = NT * ScanGeo<BF16>::ROWB;                    // a warp's rows of one tensor
+    static constexpr int STAGE = N_IN * ROWS;                                // [warps][2] stages
+    static constexpr int OFF_AB = SC_WARPS * 2 * STAGE;                      // as in the forward
+    static constexpr int OFF_BAR = OFF_AB + 2 * SC_WARPS * 512;
+    static constexpr int OFF_EX = OFF_BAR + (4 * SC_WARPS + 4 * SC_MAX_CLUSTER) * 8;
+    static constexpr int smem(int cluster) { return OFF_EX + 4 * cluster * 512; }
+};
+
+template <bool BF16, bool GATE, bool NORM>
+__global__ void __launch_bounds__(SC_THREADS, 2)
+scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
+    using K = ScanBwd<BF16, GATE>;
+    constexpr int NT = K::NT, TILE = SC_WARPS * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % cluster, ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
+    const ScanSpan sp = scan_span(a, blockIdx.y, gridDim.y, lane);
+    const int tile0 = sp.t0 / TILE, n_tiles = sp.t1 > sp.t0 ? (sp.t1 + TILE - 1) / TILE - tile0 : 0;
+    const int n_steps = (n_tiles + cluster - 1) / cluster;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + K::OFF_BAR);
+    uint64_t* const full = bars + 2 * warp;                    // this warp's loads
+    uint64_t* const given = bars + 2 * SC_WARPS + 2 * warp;    // this warp's piece
+    uint64_t* const sent = bars + 4 * SC_WARPS;                // the cluster's pieces, [4][cluster]
+    float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);
+    uint8_t* const stages = smem + warp * 2 * K::STAGE;
+    const bool even = (D & 1) == 0, tma = width == 16;
+    bool failed = false;
+
+    if (tma && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4 * SC_WARPS + 4 * cluster; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        if (cluster > 1)
+            for (int i = 0; i < 4 * cluster; ++i) mbar_arrive_expect_tx(&sent[i], 512);
     }
-    if (a.d_init) a.d_init[(size_t)n * a.D + ch] = c;
+    __syncthreads();
+    // tiles from the last one; those before the split's first (of the last step) have no tokens
+    int tw = (tile0 + n_tiles - 1 - rank) * TILE + (SC_WARPS - 1 - warp) * NT;
+    const int by = -cluster * TILE;
+    auto load = [&](int s, int t) {  // step s, whose tokens begin at t
+        uint8_t* const st = stages + (s & 1) * K::STAGE;
+        if (tma) {
+            if (lane == 0 && s < n_steps) {
+                const int y = t < 0 ? 0 : t;  // no tokens: any rows do
+                uint64_t* const b = full + (s & 1);
+                mbar_arrive_expect_tx(b, K::STAGE);
+#pragma unroll
+                for (int i = 0; i < K::N_IN; ++i) tma_load_2d(st + i * K::ROWS, &maps.m[i], ch0, y, b);
+            }
+        } else {
+            if (s < n_steps) {
+                load_rows<BF16, NT>(st, a.log_alpha, a.ld_l, t, sp.t0, sp.t1, ch0, D, width, lane);
+                load_rows<BF16, NT>(st + K::ROWS, a.x, a.ld_x, t, sp.t0, sp.t1, ch0, D, width, lane);
+                load_rows<BF16, NT>(st + 2 * K::ROWS, a.d_h, a.ld_dh, t, sp.t0, sp.t1, ch0, D, width, lane);
+                if (GATE) load_rows<BF16, NT>(st + 3 * K::ROWS, a.gate, a.ld_g, t, sp.t0, sp.t1, ch0, D, width, lane);
+            }
+            cp_commit();
+        }
+    };
+    auto kept_state = [&](int t) {  // the state before token t
+        return t >= sp.t0 && t < sp.t1 ? load2(a.chunk_states, t / SCAN_CHUNK, D, ch) : f2(0.f);
+    };
+    load(0, tw);
+    load(1, tw + by);
+    float2 kept = kept_state(tw);
+    if (cluster > 1) cluster_sync_all();  // every CTA's barriers are set up before another writes to them
+
+    ScanSeen at;
+    at.calm = 0;
+    float2 carry = f2(0.f);  // a G of the token behind this CTA's tile
+    for (int s = 0; s < n_steps; ++s, tw += by) {
+        float4* const ab = reinterpret_cast<float4*>(smem + K::OFF_AB) + (s & 1) * (SC_WARPS * 32);
+        if (s >= at.calm) at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
+        const uint32_t phase = (s >> 1) & 1;
+        // whole rows, and sequences meet at most before the first token and behind the last
+        const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
+        float2 h = kept, c_end = f2(0.f);
+        kept = kept_state(tw + by);
+        if (at.starts & 1) {
+            const int n = at.seq_start(0);
+            h = a.init ? load2(a.init, n, D, ch) : f2(0.f);
+        }
+        const bool ends_here = at.ends >> (NT - 1) & 1;
+        if (ends_here) {
+            const int n = at.seq_end(NT - 1);
+            if (a.d_final && n >= 0) c_end = load2(a.d_final, n, D, ch);
+        }
+        if (tma) {
+            failed = failed || !mbar_wait(full + (s & 1), phase, a.status);
+        } else {
+            cp_wait<1>();
+            __syncwarp();
+        }
+        const uint8_t* const st = stages + (s & 1) * K::STAGE;
+
+        // forwards: the factors of each token; then back from zero: G, and the products of the decays
+        // behind each token
+        float2 kx[NT], kl[NT], kg[NT], gs[NT], as[NT], sum = f2(0.f), c = f2(0.f);
+        auto runs = [&](auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const bool own = !EDGE || (at.own >> i & 1);
+                const float2 la = tile_at<BF16>(st, i, lane);
+                float2 x = tile_at<BF16>(st + K::ROWS, i, lane), d = scan_depth2(la);
+                if (!own) d = x = f2(0.f);
+                const ScanDecay2 a2 = scan_decay2(d);
+                const float2 A = __ffma2_rn(a2.m, f2(-1.f), f2(1.f));
+                float2 sg = f2(1.f), w = f2(1.f), r = f2(0.f);
+                if (GATE) {
+                    const float2 g = tile_at<BF16>(st + 3 * K::ROWS, i, lane), y = __fmul2_rn(g, f2(-LOG2E));
+                    const float2 q = __fadd2_rn(f2(ex2_ftz(y.x), ex2_ftz(y.y)), f2(1.f));
+                    sg = f2(rcp_ftz(q.x), rcp_ftz(q.y));
+                    if (!own) sg = f2(0.f);
+                }
+                if (NORM) {
+                    const float2 n = __fmul2_rn(a2.m, __ffma2_rn(a2.m, f2(-1.f), f2(2.f)));
+                    const float2 n1 = __fadd2_rn(n, f2(SCAN_TINY));
+                    r = f2(rsqrt_ftz(n1.x), rsqrt_ftz(n1.y));
+                    w = __fmul2_rn(n, r);
+                }
+                kx[i] = GATE && NORM ? __fmul2_rn(sg, w) : (GATE ? sg : w);
+                const float2 u = GATE || NORM ? __fmul2_rn(kx[i], x) : x;
+                if (GATE) kg[i] = __fmul2_rn(u, __ffma2_rn(sg, f2(-1.f), f2(1.f)));
+                if (EDGE && i > 0 && (at.starts >> i & 1)) {
+                    const int n = at.seq_start(i);
+                    h = a.init ? load2(a.init, n, D, ch) : f2(0.f);
+                }
+                const float2 ah = __fmul2_rn(A, h);
+                kl[i] = ah;
+                if (NORM) kl[i] = __ffma2_rn(__fmul2_rn(__fmul2_rn(A, f2(-1.f)), A), __fmul2_rn(u, __fmul2_rn(r, r)), ah);
+                if (la.x > 0.f) kl[i].x = 0.f;  // the clamp passes no gradient there
+                if (la.y > 0.f) kl[i].y = 0.f;
+                h = __fadd2_rn(ah, u);
+                as[i] = A;
+                sum = __fadd2_rn(sum, d);
+            }
+            float2 P = f2(1.f);
+#pragma unroll
+            for (int i = NT - 1; i >= 0; --i) {
+                float2 dh = tile_at<BF16>(st + 2 * K::ROWS, i, lane);
+                if (EDGE && !(at.own >> i & 1)) dh = f2(0.f);
+                if (EDGE && i < NT - 1 && (at.ends >> i & 1)) {
+                    const int n = at.seq_end(i);
+                    c = a.d_final && n >= 0 ? load2(a.d_final, n, D, ch) : f2(0.f);
+                }
+                gs[i] = __fadd2_rn(dh, c);
+                c = __fmul2_rn(as[i], gs[i]);
+                const float2 A = as[i];
+                as[i] = P;
+                P = __fmul2_rn(P, A);
+            }
+        };
+        if (plain) runs(std::false_type{});
+        else runs(std::true_type{});
+        float4 piece = scan_piece(false, sum, c);
+        if (at.ends) {  // nothing of what lies behind gets through
+            const float2 b = at.ends == 1u << (NT - 1) ? scan_fold2(piece, c_end) : c;
+            piece = make_float4(SC_CUT, SC_CUT, b.x, b.y);
+        }
+        __syncwarp();
+        if (!failed) load(s + 2, tw + 2 * by);  // into the stage that this warp has just read
+
+        // the pieces of the warps with later tokens; its own joined to them goes on
+        float4 before = make_float4(-0.f, -0.f, 0.f, 0.f);
+        if (warp > 0) {
+            failed = failed || !mbar_wait(given - 2 + (s & 1), phase, a.status);
+            before = ab[(warp - 1) * 32 + lane];
+            piece = scan_join2(before, piece);
+        }
+        if (warp < SC_WARPS - 1) {
+            ab[warp * 32 + lane] = piece;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(given + (s & 1));
+        } else {
+            const int slot = (s & 3) * cluster + rank;
+            if (cluster > 1) {
+                const uint32_t to = smem_u32(ex + slot * 32 + lane), on = smem_u32(sent + slot);
+                for (int k = 0; k < cluster; ++k) st_async16(map_to_cta(to, k), piece, map_to_cta(on, k));
+            } else {
+                ex[slot * 32 + lane] = piece;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sent + slot);
+            }
+        }
+        for (int k = 0; k < cluster; ++k) {
+            const bool last = rank + k < cluster;
+            const int r = last ? rank + k : rank + k - cluster, q = last ? s - 1 : s, slot = (q & 3) * cluster + r;
+            if (q < 0) continue;
+            const uint32_t ph = (q >> 2) & 1;
+            failed = failed || !(cluster > 1 ? mbar_wait_peers(sent + slot, ph, a.status) : mbar_wait(sent + slot, ph, a.status));
+            if (cluster > 1 && warp == 0 && lane == 0) mbar_arrive_expect_tx(sent + slot, 512);  // for step q + 4
+            const float4 v = ex[slot * 32 + lane];
+            carry = scan_fold2(v, carry, scan_is_cut(v));
+        }
+        float2 mine = warp > 0 ? scan_fold2(before, carry, scan_is_cut(before)) : carry;
+        if (ends_here) mine = c_end;
+
+        if (plain) {
+            const float2 g0 = __ffma2_rn(as[0], mine, gs[0]);
+            if (ch < D) {
+                const uint32_t es = a.out_bf16 ? 2 : 4, row = (uint32_t)D * es;
+                const size_t off = (size_t)tw * row + (size_t)ch * es;
+                uint8_t* const px = static_cast<uint8_t*>(a.dx) + off;
+                uint8_t* const pl = static_cast<uint8_t*>(a.dl) + off;
+                uint8_t* const pg = static_cast<uint8_t*>(a.dg) + off;
+                if (a.out_bf16) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const float2 G = __ffma2_rn(as[i], mine, gs[i]);
+                        const float2 x = __fmul2_rn(G, kx[i]), l = __fmul2_rn(G, kl[i]);
+                        *reinterpret_cast<uint32_t*>(px + (size_t)row * i) = pack_bf16x2(x.x, x.y);
+                        *reinterpret_cast<uint32_t*>(pl + (size_t)row * i) = pack_bf16x2(l.x, l.y);
+                        if (GATE) {
+                            const float2 g = __fmul2_rn(G, kg[i]);
+                            *reinterpret_cast<uint32_t*>(pg + (size_t)row * i) = pack_bf16x2(g.x, g.y);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const float2 G = __ffma2_rn(as[i], mine, gs[i]);
+                        *reinterpret_cast<float2*>(px + (size_t)row * i) = __fmul2_rn(G, kx[i]);
+                        *reinterpret_cast<float2*>(pl + (size_t)row * i) = __fmul2_rn(G, kl[i]);
+                        if (GATE) *reinterpret_cast<float2*>(pg + (size_t)row * i) = __fmul2_rn(G, kg[i]);
+                    }
+                }
+            }
+            if ((at.starts & 1) && a.d_init) {
+                const int n = at.seq_start(0);
+                const float2 la = tile_decay<BF16>(a.log_alpha, a.ld_l, tw, D, ch);
+                store2(a.d_init, false, n, D, ch, __fmul2_rn(la, g0));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const bool from_end = at.ends & (((1u << (NT - 1)) - 1u) & ~((1u << i) - 1u));
+                const float2 G = from_end ? gs[i] : __ffma2_rn(as[i], mine, gs[i]);
+                if (!(at.own >> i & 1)) continue;
+                store2(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
+                store2(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
+                if (GATE) store2(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
+                if ((at.starts >> i & 1) && a.d_init) {
+                    const int n = at.seq_start(i);
+                    store2(a.d_init, false, n, D, ch, __fmul2_rn(tile_decay<BF16>(a.log_alpha, a.ld_l, tw + i, D, ch), G));
+                }
+            }
+        }
+    }
+    cp_wait<0>();
+    if (failed && tma && lane == 0)  // loads still in flight
+        for (int s = n_steps < 2 ? 0 : n_steps - 2; s < n_steps; ++s) mbar_wait(full + (s & 1), (s >> 1) & 1, nullptr);
+    if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may write to it
+    // sequences without tokens
+    if (a.d_init && rank == 0) {
+        for (int n = sp.n0 + warp; n < sp.n1; n += SC_WARPS) {
+            int64_t first, end;
+            scan_range(a.cu, n, a.T, &first, &end);
+            if (first == end)
+                store2(a.d_init, false, n, D, ch, a.d_final ? load2(a.d_final, n, D, ch) : f2(0.f));
+        }
+    }
 }
 
 }  // namespace
@@ -63,15 +294,20 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, bool own_states, cudaStream_t str
     } else if (a.status && (e = launch_scan_check(a, stream)) != cudaSuccess) {
         return e;
     }
-    const dim3 grid((a.D + 127) / 128, a.n_seqs);
-    if (a.gate) {
-        if (a.normalize) scan_bwd_kernel<true, true><<<grid, 128, 0, stream>>>(a);
-        else scan_bwd_kernel<true, false><<<grid, 128, 0, stream>>>(a);
-    } else {
-        if (a.normalize) scan_bwd_kernel<false, true><<<grid, 128, 0, stream>>>(a);
-        else scan_bwd_kernel<false, false><<<grid, 128, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    const void* in[] = {a.log_alpha, a.x, a.d_h, a.gate};
+    const int64_t ld[] = {a.ld_l, a.ld_x, a.ld_dh, a.ld_g};
+    ScanMaps maps;
+    int width = 0;
+    if ((e = scan_maps(a, in, ld, a.gate ? 4 : 3, SCAN_CHUNK, &maps, &width)) != cudaSuccess) return e;
+    KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
+        if (a.in_bf16)
+            e = scan_launch<scan_bwd_kernel<true, G, W>>(ScanBwd<true, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width,
+                                                         stream);
+        else
+            e = scan_launch<scan_bwd_kernel<false, G, W>>(ScanBwd<false, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width,
+                                                          stream);
+    });
+    return e;
 }
 
 }  // namespace kda

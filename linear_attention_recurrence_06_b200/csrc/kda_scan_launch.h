@@ -9,13 +9,25 @@
 
 namespace kda {
 
+// __VA_ARGS__ with the constants G (a gate) and W (normalize)
+#define KDA_SCAN_GN(GATE, NORM, ...)                                     \
+    do {                                                                 \
+        if (GATE) {                                                      \
+            if (NORM) { constexpr bool G = true, W = true; __VA_ARGS__; }       \
+            else      { constexpr bool G = true, W = false; __VA_ARGS__; }      \
+        } else {                                                         \
+            if (NORM) { constexpr bool G = false, W = true; __VA_ARGS__; }      \
+            else      { constexpr bool G = false, W = false; __VA_ARGS__; }     \
+        }                                                                \
+    } while (0)
+
 // [rows, cols] tensor, rows `ld` elements apart, box of a warp's tokens, zeros outside
-bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, bool bf16);
+bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool bf16);
 
 // The widest copy that every input's address and token stride allow (16: TMA), and the tensor
 // maps for it.
-inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int64_t* ld, int n, ScanMaps* maps,
-                             int* width) {
+inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int64_t* ld, int n, int box_rows,
+                             ScanMaps* maps, int* width) {
     memset(maps, 0, sizeof(*maps));
     const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
     uintptr_t all = 0;
@@ -23,7 +35,7 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
     *width = all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
     if (*width == 16 && tokens > 0)
         for (int i = 0; i < n; ++i)
-            if (!make_scan_map(&maps->m[i], in[i], tokens, a.D, ld[i], a.in_bf16)) return cudaErrorInvalidValue;
+            if (!make_scan_map(&maps->m[i], in[i], tokens, a.D, ld[i], box_rows, a.in_bf16)) return cudaErrorInvalidValue;
     return cudaSuccess;
 }
 

@@ -29,11 +29,7 @@ constexpr int SC_MAX_CLUSTER = 8;   // the portable limit
 template <bool BF16>
 struct ScanGeo {
     static constexpr int ES = BF16 ? 2 : 4;
-    static constexpr int NT = BF16 ? 16 : 8;      // tokens of a warp: 16 KB per tensor and tile
-    static constexpr int TILE = SC_WARPS * NT;
     static constexpr int ROWB = SC_CH * ES;       // bytes of a tile's row
-    static constexpr int TENS = TILE * ROWB;      // bytes of one tensor's tile
-    static_assert(SCAN_CHUNK % NT == 0 && TILE % SCAN_CHUNK == 0, "a chunk starts with a warp's tokens");
 };
 
 // ---- two channels at a time
@@ -128,14 +124,14 @@ KDA_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); 
 template <int N>
 KDA_DEV void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <bool BF16>
+template <bool BF16, int NT>
 __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t ld, int tw, int t0, int t1, int ch0, int D,
                                        int width, int lane) {
     using Geo = ScanGeo<BF16>;
     constexpr int ES = Geo::ES;
     uint8_t* const rows = dst;
     const uint8_t* const src = static_cast<const uint8_t*>(base);
-    for (int i = 0; i < Geo::NT; ++i) {
+    for (int i = 0; i < NT; ++i) {
         const int t = tw + i;
         const bool row_in = t >= t0 && t < t1;
         if (!BF16 || width == 4) {
@@ -169,7 +165,7 @@ KDA_DEV float2 tile_at(const uint8_t* tile, int row, int lane) {
 }
 
 // Two channels of a row of an output [tokens, D].
-__device__ __noinline__ void store2(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
+static __device__ __noinline__ void store2(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
     const size_t i = row * D + ch;
     if (ch + 1 < D && (D & 1) == 0) {
         if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + i) = pack_bf16x2(v.x, v.y);
@@ -184,6 +180,13 @@ __device__ __noinline__ void store2(void* base, bool bf16, size_t row, int D, in
         if (bf16) static_cast<uint16_t*>(base)[i + 1] = f32_to_bf16(v.y);
         else static_cast<float*>(base)[i + 1] = v.y;
     }
+}
+// The decays of a token's channels ch, ch + 1 from global memory (for the few that begin a sequence).
+template <bool BF16>
+__device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
+    const size_t i = (size_t)t * ld + ch;
+    const float2 d = scan_depth2(f2(ch < D ? ld_in<BF16>(log_alpha, i) : 0.f, ch + 1 < D ? ld_in<BF16>(log_alpha, i + 1) : 0.f));
+    return __ffma2_rn(scan_decay2(d).m, f2(-1.f), f2(1.f));
 }
 KDA_DEV float2 load2(const float* base, size_t row, int D, int ch) {
     const size_t i = row * D + ch;

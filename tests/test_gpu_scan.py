@@ -229,7 +229,7 @@ def test_guards_and_in_place_state():
     T, D = 130, 65
     i = inputs(53, 2, T, D, BF)
     h, ok_h = guarded_empty((2, T, D), BF)
-    cs, ok_c = guarded_empty((-(-2 * T // 64), D), F32)
+    cs, ok_c = guarded_empty((-(-2 * T // kda.SCAN_CHUNK), D), F32)
     state, ok_s = guarded_empty((2, D), F32)
     state.copy_(i["init"])
     r = kda.scan_fwd(i["x"], i["la"], state, gate=i["gate"], out=h, final_state=state, chunk_states=cs)
