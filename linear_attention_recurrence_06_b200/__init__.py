@@ -26,7 +26,6 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -468,6 +467,11 @@ def _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, nor
     _check_cuda(q)
     if q.dim() != 4:
         raise ValueError("q must be [n, Bd, H, 128]")
+    there = _elsewhere(q, stream)
+    if there is not None:
+        with there:
+            return _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, norm_weight, eps, out_dtype,
+                                       out, step_states, None)
     n, Bd, H, dk = q.shape
     dv = v.shape[-1]
     rows = (n, Bd, H)
@@ -477,20 +481,18 @@ def _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, nor
                            (beta, rows, "beta"), (gate, rows + (dv,), "gate")):
         _check_like(q, q.dtype, shape, name, t)
     _check_like(q, torch.float32, (dv,), "norm_weight", norm_weight)
-    odt = out_dtype if out_dtype is not None else (q.dtype if out is None else out.dtype)
-    want = step_states is not None
-    with _on(q, stream):
-        o = out if out is not None else torch.empty(rows + (dv,), dtype=odt, device=q.device)
-        if step_states is True:
-            step_states = torch.empty(rows + (dk, dv), dtype=torch.float32, device=q.device)
-        if out is not None:
-            _check_like(q, odt, rows + (dv,), "out", out)
-        if want:
-            _check_like(q, torch.float32, rows + (dk, dv), "step_states", step_states)
-        st = load_library().kda_decode_steps_paged(_ptr(state), _ptr(slots), state.shape[0], _ptr(q), _ptr(k), _ptr(v),
-                                                   _ptr(log_alpha), _ptr(beta), _ptr(o), n, Bd, H, dk, dv, _dt(q),
-                                                   _dt(o), float(scale), _ptr(gate), _ptr(norm_weight), float(eps),
-                                                   _ptr(step_states), _stream(None))
+    o, want = out, step_states is not None
+    if o is None:
+        o = torch.empty(v.shape, dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+    else:
+        _check_like(q, out_dtype if out_dtype is not None else o.dtype, rows + (dv,), "out", o)
+    if step_states is True:
+        step_states = torch.empty(rows + (dk, dv), dtype=torch.float32, device=q.device)
+    _check_like(q, torch.float32, rows + (dk, dv), "step_states", step_states)
+    st = load_library().kda_decode_steps_paged(_at(state), _at(slots), state.shape[0], _at(q), _at(k), _at(v),
+                                               _at(log_alpha), _at(beta), _at(o), n, Bd, H, dk, dv, _dt(q), _dt(o),
+                                               scale, _at(gate), _at(norm_weight), eps, _at(step_states),
+                                               _here(q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_steps_paged")
     return (o, step_states) if want else o
@@ -511,31 +513,40 @@ def gate_norm(o, g, norm_weight=None, *, eps: float = 1e-6, out_dtype=None, out=
     return y
 
 
-def _on(t, stream):
-    """Context in which a call on tensor t runs: its device current, and `stream`
-    (of that device) the current stream, so that what the call allocates belongs to it."""
+def _elsewhere(t, stream):
+    """None where a call on tensor t can run as things are; else the context for it: its
+    device current, and `stream` (of that device) the current stream, so that what the
+    call allocates belongs to it."""
     torch = _torch()
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    if t.get_device() == torch.cuda.current_device():
+        return None
+    return torch.cuda.device(t.device)
+
+
+def _here(device_index):
+    """The current stream of the current device, as the library takes it."""
+    return _torch()._C._cuda_getCurrentRawStream(device_index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_like(x, dtype, shape, name, t):
-    """t: a contiguous tensor of this dtype and shape on x's device."""
-    if t is None:
+    """t: None, or a contiguous tensor of this dtype and shape on x's device."""
+    if t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.get_device() == x.get_device()):
         return
     if not t.is_cuda or t.device != x.device:
         raise ValueError(f"{name} must be a CUDA tensor on {x.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _check_slots(x, slots, name, n=None):
@@ -573,7 +584,6 @@ def _token_rows(x, t, name):
 
 
 def _scan_dims(x, cu_seqlens, initial_state):
-    torch = _torch()
     if not x.is_cuda:
         raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
     if x.dim() < 3:
@@ -584,7 +594,8 @@ def _scan_dims(x, cu_seqlens, initial_state):
     if cu_seqlens is not None:
         _check_slots(x, cu_seqlens, "cu_seqlens")
         N = cu_seqlens.numel() - 1
-    _check_like(x, torch.float32, (N,) + ch, "initial_state", initial_state)
+    if initial_state is not None:
+        _check_like(x, _torch().float32, (N,) + ch, "initial_state", initial_state)
     return B, T, ch, math.prod(ch), N
 
 
@@ -600,32 +611,37 @@ def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = F
     ([N, H, d]) or None.  Varlen: B = 1 and cu_seqlens int32 [N+1] on the device;
     rows of tokens behind cu_seqlens[N] are left as they are.
     Returns (h, final_state fp32 [N, D] or None); with chunk_states (True: allocate)
-    also those, for scan_bwd.  workspace: optional, for query_status."""
+    also those, fp32 [ceil(B T / 8), D], for scan_bwd.  workspace: optional, for
+    query_status."""
     torch = _torch()
     B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
-    ld = [_token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha"),
-          0 if gate is None else _token_rows(x, gate, "gate")]
-    odt = out_dtype if out_dtype is not None else (x.dtype if out is None else out.dtype)
-    n_chunks = -(-B * T // SCAN_CHUNK)
-    with _on(x, stream):
-        h = out if out is not None else torch.empty(x.shape, dtype=odt, device=x.device)
-        fs = final_state
-        if fs is None and output_final_state:
-            fs = torch.empty((N,) + ch, dtype=torch.float32, device=x.device)
-        want = chunk_states is not None
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return scan_fwd(x, log_alpha, initial_state, gate=gate, normalize=normalize, cu_seqlens=cu_seqlens,
+                            out_dtype=out_dtype, output_final_state=output_final_state, final_state=final_state,
+                            out=out, chunk_states=chunk_states, workspace=workspace)
+    ldx, ldl = _token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha")
+    ldg = 0 if gate is None else _token_rows(x, gate, "gate")
+    h, fs, want = out, final_state, chunk_states is not None
+    if h is None:
+        h = torch.empty(x.shape, dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
+    else:
+        _check_like(x, out_dtype if out_dtype is not None else h.dtype, x.shape, "out", h)
+    if fs is not None:
+        _check_like(x, torch.float32, (N,) + ch, "final_state", fs)
+    elif output_final_state:
+        fs = torch.empty((N,) + ch, dtype=torch.float32, device=x.device)
+    if want:
+        shape = (-(-B * T // SCAN_CHUNK),) + ch
         if chunk_states is True:
-            chunk_states = torch.empty((n_chunks,) + ch, dtype=torch.float32, device=x.device)
-        if out is not None:
-            _check_like(x, odt, x.shape, "out", out)
-        if final_state is not None:
-            _check_like(x, torch.float32, (N,) + ch, "final_state", fs)
-        if want:
-            _check_like(x, torch.float32, (n_chunks,) + ch, "chunk_states", chunk_states)
-        _check_cuda(workspace)
-        st = load_library().kda_scan_fwd(_ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(initial_state), _ptr(h), _ptr(fs),
-                                         _ptr(chunk_states), B, T, D, *ld, _ptr(cu_seqlens), N, _dt(x), _dt(h),
-                                         int(normalize), _ptr(workspace),
-                                         0 if workspace is None else workspace.numel(), _stream(None))
+            chunk_states = torch.empty(shape, dtype=torch.float32, device=x.device)
+        _check_like(x, torch.float32, shape, "chunk_states", chunk_states)
+    _check_cuda(workspace)
+    st = load_library().kda_scan_fwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(h), _at(fs),
+                                     _at(chunk_states), B, T, D, ldx, ldl, ldg, _at(cu_seqlens), N, _dt(x), _dt(h),
+                                     int(normalize), _at(workspace), 0 if workspace is None else workspace.numel(),
+                                     _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_fwd")
     return (h, fs, chunk_states) if want else (h, fs)
@@ -651,24 +667,29 @@ def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=
     not wanted)."""
     torch = _torch()
     B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
-    ld = [_token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha"),
-          0 if gate is None else _token_rows(x, gate, "gate"), _token_rows(x, d_h, "d_h")]
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return scan_bwd(x, log_alpha, d_h, initial_state, d_final_state, gate=gate, normalize=normalize,
+                            cu_seqlens=cu_seqlens, chunk_states=chunk_states, out_dtype=out_dtype,
+                            want_d_initial_state=want_d_initial_state, workspace=workspace)
+    ld = (_token_rows(x, x, "x"), _token_rows(x, log_alpha, "log_alpha"),
+          0 if gate is None else _token_rows(x, gate, "gate"), _token_rows(x, d_h, "d_h"))
     _check_like(x, torch.float32, (N,) + ch, "d_final_state", d_final_state)
     _check_like(x, torch.float32, (-(-B * T // SCAN_CHUNK),) + ch, "chunk_states", chunk_states)
     odt = out_dtype if out_dtype is not None else torch.float32
-    with _on(x, stream):
-        g = {k: torch.empty(x.shape, dtype=odt, device=x.device) for k in ("dx", "dlog_alpha")}
-        g["dgate"] = None if gate is None else torch.empty(x.shape, dtype=odt, device=x.device)
-        g["d_initial_state"] = torch.empty((N,) + ch, dtype=torch.float32, device=x.device) \
-            if want_d_initial_state else None
-        if workspace is None and chunk_states is None:
-            workspace = torch.empty(scan_bwd_workspace_size(B, T, D), dtype=torch.uint8, device=x.device)
-        _check_cuda(workspace)
-        st = load_library().kda_scan_bwd(_ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(initial_state), _ptr(d_h),
-                                         _ptr(d_final_state), _ptr(chunk_states), _ptr(g["dx"]),
-                                         _ptr(g["dlog_alpha"]), _ptr(g["dgate"]), _ptr(g["d_initial_state"]), B, T, D,
-                                         *ld, _ptr(cu_seqlens), N, _dt(x), _dt(g["dx"]), int(normalize),
-                                         _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(None))
+    g = {k: torch.empty(x.shape, dtype=odt, device=x.device) for k in ("dx", "dlog_alpha")}
+    g["dgate"] = None if gate is None else torch.empty(x.shape, dtype=odt, device=x.device)
+    g["d_initial_state"] = torch.empty((N,) + ch, dtype=torch.float32, device=x.device) \
+        if want_d_initial_state else None
+    if workspace is None and chunk_states is None:
+        workspace = torch.empty(scan_bwd_workspace_size(B, T, D), dtype=torch.uint8, device=x.device)
+    _check_cuda(workspace)
+    st = load_library().kda_scan_bwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(d_h),
+                                     _at(d_final_state), _at(chunk_states), _at(g["dx"]), _at(g["dlog_alpha"]),
+                                     _at(g["dgate"]), _at(g["d_initial_state"]), B, T, D, *ld, _at(cu_seqlens), N,
+                                     _dt(x), _dt(g["dx"]), int(normalize), _at(workspace),
+                                     0 if workspace is None else workspace.numel(), _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_bwd")
     return g
@@ -684,28 +705,32 @@ def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False
     (allocate) or fp32 [n, Bd, D] receiving the state after every token.
     Returns h [n, Bd, D], or (h, step_states)."""
     torch = _torch()
-    _check_cuda(state, x, log_alpha, gate)
+    _check_cuda(x)
     if x.dim() < 3:
         raise ValueError("x must be [n, Bd, D] (or [n, Bd, H, d])")
-    for t, name in ((log_alpha, "log_alpha"), (gate, "gate")):
-        _check_like(x, x.dtype, x.shape, name, t)
-    n, Bd = x.shape[0], x.shape[1]
-    ch = tuple(x.shape[2:])
-    _check_like(x, torch.float32, (state.shape[0],) + ch, "state", state)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return scan_decode_steps(state, x, log_alpha, gate=gate, normalize=normalize, slots=slots,
+                                     out_dtype=out_dtype, out=out, step_states=step_states)
+    shape = x.shape
+    _check_like(x, x.dtype, shape, "log_alpha", log_alpha)
+    _check_like(x, x.dtype, shape, "gate", gate)
+    n, Bd = shape[0], shape[1]
+    ch, P = tuple(shape[2:]), state.shape[0]
+    _check_like(x, torch.float32, (P,) + ch, "state", state)
     _check_slots(x, slots, "slots", Bd)
-    odt = out_dtype if out_dtype is not None else (x.dtype if out is None else out.dtype)
-    want = step_states is not None
-    with _on(x, stream):
-        h = out if out is not None else torch.empty(x.shape, dtype=odt, device=x.device)
-        if step_states is True:
-            step_states = torch.empty(x.shape, dtype=torch.float32, device=x.device)
-        if out is not None:
-            _check_like(x, odt, x.shape, "out", out)
-        if want:
-            _check_like(x, torch.float32, x.shape, "step_states", step_states)
-        st = load_library().kda_scan_decode_steps(_ptr(state), _ptr(x), _ptr(log_alpha), _ptr(gate), _ptr(h),
-                                                  _ptr(slots), state.shape[0], n, Bd, math.prod(ch), _dt(x), _dt(h),
-                                                  int(normalize), _ptr(step_states), _stream(None))
+    h, want = out, step_states is not None
+    if h is None:
+        h = torch.empty(shape, dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
+    else:
+        _check_like(x, out_dtype if out_dtype is not None else h.dtype, shape, "out", h)
+    if step_states is True:
+        step_states = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _check_like(x, torch.float32, shape, "step_states", step_states)
+    st = load_library().kda_scan_decode_steps(_at(state), _at(x), _at(log_alpha), _at(gate), _at(h), _at(slots), P, n,
+                                              Bd, math.prod(ch), _dt(x), _dt(h), int(normalize), _at(step_states),
+                                              _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_decode_steps")
     return (h, step_states) if want else h
@@ -726,29 +751,31 @@ def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=N
     d_o, d_gate (o's shape, fp32 or out_dtype) and d_norm_weight fp32 [128] (None when not
     wanted; without a norm_weight the gradient at a weight of ones)."""
     torch = _torch()
-    _check_cuda(o, g, d_y, norm_weight, workspace)
+    _check_cuda(o, workspace)
     if o.shape[-1] != HEAD_DIM:
         raise KdaError(-2, "kda_gate_norm_bwd")
-    for t, name in ((g, "g"), (d_y, "d_y")):
-        _check_like(o, o.dtype, o.shape, name, t)
+    there = _elsewhere(o, stream)
+    if there is not None:
+        with there:
+            return gate_norm_bwd(o, g, d_y, norm_weight, eps=eps, out_dtype=out_dtype,
+                                 want_d_norm_weight=want_d_norm_weight, workspace=workspace)
+    _check_like(o, o.dtype, o.shape, "g", g)
+    _check_like(o, o.dtype, o.shape, "d_y", d_y)
     _check_like(o, torch.float32, (HEAD_DIM,), "norm_weight", norm_weight)
     rows = o.numel() // HEAD_DIM
-    odt = out_dtype if out_dtype is not None else torch.float32
-    with _on(o, stream):
-        r = dict(d_o=torch.empty(o.shape, dtype=odt, device=o.device),
-                 d_gate=torch.empty(o.shape, dtype=odt, device=o.device),
-                 d_norm_weight=torch.empty(HEAD_DIM, dtype=torch.float32, device=o.device)
-                 if want_d_norm_weight else None)
-        if workspace is None and want_d_norm_weight:
-            n = ctypes.c_size_t(0)
-            st = load_library().kda_gate_norm_bwd_workspace_size(rows, HEAD_DIM, ctypes.byref(n))
-            if st != KDA_OK:
-                raise KdaError(st, "kda_gate_norm_bwd_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=o.device)
-        st = load_library().kda_gate_norm_bwd(_ptr(o), _ptr(g), _ptr(d_y), _ptr(norm_weight), float(eps),
-                                              _ptr(r["d_o"]), _ptr(r["d_gate"]), _ptr(r["d_norm_weight"]), rows,
-                                              HEAD_DIM, _dt(o), _dt(r["d_o"]), _ptr(workspace),
-                                              0 if workspace is None else workspace.numel(), _stream(None))
+    odt, dev = out_dtype if out_dtype is not None else torch.float32, o.device
+    r = dict(d_o=torch.empty(o.shape, dtype=odt, device=dev), d_gate=torch.empty(o.shape, dtype=odt, device=dev),
+             d_norm_weight=torch.empty(HEAD_DIM, dtype=torch.float32, device=dev) if want_d_norm_weight else None)
+    if workspace is None and want_d_norm_weight:
+        n = ctypes.c_size_t(0)
+        st = load_library().kda_gate_norm_bwd_workspace_size(rows, HEAD_DIM, ctypes.byref(n))
+        if st != KDA_OK:
+            raise KdaError(st, "kda_gate_norm_bwd_workspace_size")
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    st = load_library().kda_gate_norm_bwd(_at(o), _at(g), _at(d_y), _at(norm_weight), eps, _at(r["d_o"]),
+                                          _at(r["d_gate"]), _at(r["d_norm_weight"]), rows, HEAD_DIM, _dt(o),
+                                          _dt(r["d_o"]), _at(workspace),
+                                          0 if workspace is None else workspace.numel(), _here(o.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_gate_norm_bwd")
     return r
@@ -778,18 +805,23 @@ def state_copy(dst, dst_slots, src, src_slots, *, layered: bool = False, stream=
         raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
     _check_slots(dst, dst_slots, "dst_slots")
     _check_slots(dst, src_slots, "src_slots", dst_slots.numel())
+    there = _elsewhere(dst, stream)
+    if there is not None:
+        with there:
+            return state_copy(dst, dst_slots, src, src_slots, layered=layered)
     L, P, page, d_layer = _pool_dims(dst, layered, "dst")
     Q, s_layer = 0, 0
-    if src is not None:
+    if src is dst:
+        Q, s_layer = P, d_layer
+    elif src is not None:
         if src.dtype != dst.dtype or src.shape[1 + layered:] != dst.shape[1 + layered:] or \
                 (layered and src.shape[0] != L):
             raise ValueError("dst and src must have one dtype, page shape and number of layers")
         _, Q, _, s_layer = _pool_dims(src, layered, "src")
     if page == 0:
         return dst
-    with _on(dst, stream):
-        st = load_library().kda_state_copy(_ptr(dst), _ptr(src), L, page, P, Q, d_layer, s_layer, _ptr(dst_slots),
-                                           _ptr(src_slots), dst_slots.numel(), _stream(None))
+    st = load_library().kda_state_copy(_at(dst), _at(src), L, page, P, Q, d_layer, s_layer, _at(dst_slots),
+                                       _at(src_slots), dst_slots.numel(), _here(dst.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_state_copy")
     return dst
@@ -807,9 +839,12 @@ def state_alloc(live, n: int, *, stream=None):
     device) and returns them as int32 [n], -1 where no slot was left."""
     torch = _torch()
     _check_live(live)
-    with _on(live, stream):
-        slots = torch.empty(n, dtype=torch.int32, device=live.device)
-        st = load_library().kda_state_alloc(_ptr(live), live.numel(), _ptr(slots), n, _stream(None))
+    there = _elsewhere(live, stream)
+    if there is not None:
+        with there:
+            return state_alloc(live, n)
+    slots = torch.empty(n, dtype=torch.int32, device=live.device)
+    st = load_library().kda_state_alloc(_at(live), live.numel(), _at(slots), n, _here(live.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_state_alloc")
     return slots
@@ -819,8 +854,11 @@ def state_free(live, slots, *, stream=None):
     """Marks slots (int32, on the device; those out of range are ignored) free in live."""
     _check_live(live)
     _check_slots(live, slots, "slots")
-    with _on(live, stream):
-        st = load_library().kda_state_free(_ptr(live), live.numel(), _ptr(slots), slots.numel(), _stream(None))
+    there = _elsewhere(live, stream)
+    if there is not None:
+        with there:
+            return state_free(live, slots)
+    st = load_library().kda_state_free(_at(live), live.numel(), _at(slots), slots.numel(), _here(live.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_state_free")
 
@@ -832,12 +870,15 @@ def state_compact(live, *, stream=None):
     new_slots [P] (where each old slot's page lies now, -1 if free) and n_live [1]."""
     torch = _torch()
     _check_live(live)
+    there = _elsewhere(live, stream)
+    if there is not None:
+        with there:
+            return state_compact(live)
     P = live.numel()
-    with _on(live, stream):
-        r = {k: torch.empty(P, dtype=torch.int32, device=live.device) for k in ("dst_slots", "src_slots", "new_slots")}
-        r["n_live"] = torch.empty(1, dtype=torch.int32, device=live.device)
-        st = load_library().kda_state_compact(_ptr(live), P, _ptr(r["dst_slots"]), _ptr(r["src_slots"]),
-                                              _ptr(r["new_slots"]), _ptr(r["n_live"]), _stream(None))
+    r = {k: torch.empty(P, dtype=torch.int32, device=live.device) for k in ("dst_slots", "src_slots", "new_slots")}
+    r["n_live"] = torch.empty(1, dtype=torch.int32, device=live.device)
+    st = load_library().kda_state_compact(_at(live), P, _at(r["dst_slots"]), _at(r["src_slots"]), _at(r["new_slots"]),
+                                          _at(r["n_live"]), _here(live.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_state_compact")
     return r

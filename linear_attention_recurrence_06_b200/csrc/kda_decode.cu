@@ -62,8 +62,8 @@ decode_step_kernel(float* __restrict__ state, const void* __restrict__ q, const 
 
     size_t page = bh;  // of one head
     if constexpr (PAGED) {
-        const int slot = row_slot(slots, n_slots, bh / H);
-        if (slot < 0) {
+        const int slot = slots[bh / H];
+        if (!slot_in_range(slot, n_slots)) {
             zero_row<OUT_BF16, 256>(o, step_states, n_steps, BH, bh, 0, D);
             return;
         }
@@ -74,6 +74,12 @@ decode_step_kernel(float* __restrict__ state, const void* __restrict__ q, const 
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         st[i] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)(r0 + 8 * i) * D + col));
+    if constexpr (PAGED) {
+        if (slot_taken(slots, slots[bh / H], bh / H)) {
+            zero_row<OUT_BF16, 256>(o, step_states, n_steps, BH, bh, 0, D);
+            return;
+        }
+    }
 
     // this step's token values, loaded one step ahead into registers
     float nk = 0.f, nq = 0.f, nla = 0.f, nb, nv[4], ng[4];
@@ -261,8 +267,8 @@ decode_multi_kernel(float* __restrict__ state, const void* __restrict__ q, const
     };
     size_t page = bh;  // of one head
     if constexpr (PAGED) {
-        const int slot = row_slot(slots, n_slots, bh / H);
-        if (slot < 0) {
+        const int slot = slots[bh / H];
+        if (!slot_in_range(slot, n_slots)) {
             zero_row<OUT_BF16, 128>(o, step_states, n_steps, BH, bh, 64 * sl, 64);
             return;
         }
@@ -274,6 +280,13 @@ decode_multi_kernel(float* __restrict__ state, const void* __restrict__ q, const
     float2 st[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) st[i] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)(row0 + i) * D + col));
+    if constexpr (PAGED) {
+        if (slot_taken(slots, slots[bh / H], bh / H)) {
+            cp_async_wait_all();
+            zero_row<OUT_BF16, 128>(o, step_states, n_steps, BH, bh, 64 * sl, 64);
+            return;
+        }
+    }
 
     const int vc = col - 64 * sl;  // this thread's v columns within the CTA's half
     for (int t = 0; t < n_steps; ++t) {

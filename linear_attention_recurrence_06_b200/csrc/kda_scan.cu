@@ -265,29 +265,87 @@ __global__ void scan_check_cu_kernel(const int32_t* cu, int n_seqs, int64_t T, u
     if (__syncthreads_or(bad) && threadIdx.x == 0) *status = 2u;
 }
 
-template <bool GATE, bool NORM>
-__global__ void __launch_bounds__(128)
-scan_decode_kernel(float* state, const void* x, const void* log_alpha, const void* gate, void* hout,
-                   const int32_t* slots, int n_slots, int n_steps, int Bd, int D, bool in_bf16, bool out_bf16,
-                   float* step_states) {
-    const int ch = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
-    const int slot = slots ? row_slot(slots, n_slots, b) : b;
-    if (ch >= D) return;
-    float h = slot >= 0 ? state[(size_t)slot * D + ch] : 0.f;
-    for (int t = 0; t < n_steps; ++t) {
-        const size_t i = ((size_t)t * Bd + b) * D + ch;
-        if (slot >= 0) {
-            const float xv = in_bf16 ? ld_in<true>(x, i) : ld_in<false>(x, i);
-            const float l = in_bf16 ? ld_in<true>(log_alpha, i) : ld_in<false>(log_alpha, i);
-            const float g = !GATE ? 0.f : in_bf16 ? ld_in<true>(gate, i) : ld_in<false>(gate, i);
-            const ScanTerm r = scan_term<GATE, NORM>(xv, l, g);
-            h = scan_step(r.p, h, r.u);
-        }
-        if (out_bf16) st_out<true>(hout, i, h);
-        else st_out<false>(hout, i, h);
-        if (step_states) step_states[i] = h;
+// Single tokens: V channels of one row per thread (4 where D allows 16-byte states), the state read
+// and written once for all steps of a call.  HBM-bound for many rows, else latency: the row's
+// slot, its state and the first tokens are on their way before the slot is checked against the
+// rows before it, and every step's tokens are loaded a step ahead.
+template <bool BF16, int V>
+KDA_DEV void load_v(const void* base, size_t i, float* v) {
+    if constexpr (V == 1) {
+        v[0] = ld_in<BF16>(base, i);
+    } else if constexpr (BF16) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i));
+        v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     }
-    if (slot >= 0) state[(size_t)slot * D + ch] = h;
+}
+template <int V>
+KDA_DEV void store_v(void* base, bool bf16, size_t i, const float* v) {
+    if (bf16) {
+        uint16_t* const p = static_cast<uint16_t*>(base) + i;
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else p[0] = f32_to_bf16(v[0]);
+    } else {
+        float* const p = static_cast<float*>(base) + i;
+        if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        else p[0] = v[0];
+    }
+}
+
+template <bool BF16, bool GATE, bool NORM, int V>
+__global__ void __launch_bounds__(128)
+scan_decode_kernel(float* state, const void* __restrict__ x, const void* __restrict__ log_alpha,
+                   const void* __restrict__ gate, void* hout, const int32_t* __restrict__ slots, int n_slots,
+                   int n_steps, int Bd, int D, bool out_bf16, float* step_states) {
+    const int ch = (blockIdx.x * 128 + threadIdx.x) * V, b = blockIdx.y;
+    const bool mine = ch < D;
+    const int slot = slots ? slots[b] : b;
+    const bool there = !slots || slot_in_range(slot, n_slots);
+    const size_t row = (size_t)Bd * D, at = (size_t)b * D + ch;
+    float h[V], xv[V], lv[V], gv[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = xv[k] = lv[k] = gv[k] = 0.f;
+    auto tokens = [&](int t) {
+        const size_t i = t * row + at;
+        load_v<BF16, V>(log_alpha, i, lv);
+        load_v<BF16, V>(x, i, xv);
+        if (GATE) load_v<BF16, V>(gate, i, gv);
+    };
+    float* const S = state + (size_t)(there ? slot : 0) * D + ch;
+    if (there && mine) {
+        if constexpr (V == 4) {
+            const float4 w = *reinterpret_cast<const float4*>(S);
+            h[0] = w.x, h[1] = w.y, h[2] = w.z, h[3] = w.w;
+        } else {
+            h[0] = S[0];
+        }
+        tokens(0);
+    }
+    const bool live = slots ? !slot_taken(slots, slot, b) && there : true;
+    if (!mine) return;
+    for (int t = 0; t < n_steps; ++t) {
+        const size_t i = t * row + at;
+        if (live) {
+            float p[V], u[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const ScanTerm r = scan_term<GATE, NORM>(xv[k], lv[k], gv[k]);
+                p[k] = r.p, u[k] = r.u;
+            }
+            if (t + 1 < n_steps) tokens(t + 1);
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[k] = scan_step(p[k], h[k], u[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[k] = 0.f;
+        }
+        store_v<V>(hout, out_bf16, i, h);
+        if (step_states) store_v<V>(step_states, false, i, h);
+    }
+    if (live) store_v<V>(state, false, (size_t)slot * D + ch, h);
 }
 
 }  // namespace
@@ -324,10 +382,16 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream) {
 cudaError_t launch_scan_decode(float* state, const void* x, const void* log_alpha, const void* gate, void* h,
                                const int32_t* slots, int n_slots, int n_steps, int Bd, int D, bool in_bf16,
                                bool out_bf16, bool normalize, float* step_states, cudaStream_t stream) {
-    const dim3 grid((D + 127) / 128, Bd);
-    KDA_SCAN_GN(gate != nullptr, normalize,
-                (scan_decode_kernel<G, W><<<grid, 128, 0, stream>>>(state, x, log_alpha, gate, h, slots, n_slots,
-                                                                    n_steps, Bd, D, in_bf16, out_bf16, step_states)));
+    const bool four = D % 4 == 0;  // the tensors are 16-byte aligned
+    const dim3 grid((D + (four ? 511 : 127)) / (four ? 512 : 128), Bd);
+#define KDA_SCAN_DEC(BF, V)                                                                                       \
+    scan_decode_kernel<BF, G, W, V><<<grid, 128, 0, stream>>>(state, x, log_alpha, gate, h, slots, n_slots, n_steps, \
+                                                              Bd, D, out_bf16, step_states)
+    KDA_SCAN_GN(gate != nullptr, normalize, {
+        if (in_bf16) { if (four) KDA_SCAN_DEC(true, 4); else KDA_SCAN_DEC(true, 1); }
+        else         { if (four) KDA_SCAN_DEC(false, 4); else KDA_SCAN_DEC(false, 1); }
+    });
+#undef KDA_SCAN_DEC
     return cudaGetLastError();
 }
 
