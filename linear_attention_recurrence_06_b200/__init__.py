@@ -27,6 +27,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -146,9 +147,15 @@ def load_library(path: str | None = None):
     return lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t) -> int:
@@ -483,11 +490,11 @@ def _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, nor
     _check_like(q, torch.float32, (dv,), "norm_weight", norm_weight)
     o, want = out, step_states is not None
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+        o = _empty(v, v.shape, out_dtype)
     else:
         _check_like(q, out_dtype if out_dtype is not None else o.dtype, rows + (dv,), "out", o)
     if step_states is True:
-        step_states = torch.empty(rows + (dk, dv), dtype=torch.float32, device=q.device)
+        step_states = _empty(q, rows + (dk, dv), torch.float32)
     _check_like(q, torch.float32, rows + (dk, dv), "step_states", step_states)
     st = load_library().kda_decode_steps_paged(_at(state), _at(slots), state.shape[0], _at(q), _at(k), _at(v),
                                                _at(log_alpha), _at(beta), _at(o), n, Bd, H, dk, dv, _dt(q), _dt(o),
@@ -530,6 +537,13 @@ def _elsewhere(t, stream):
 def _here(device_index):
     """The current stream of the current device, as the library takes it."""
     return _torch()._C._cuda_getCurrentRawStream(device_index)
+
+
+def _empty(x, shape, dtype):
+    """A new contiguous tensor beside x (dtype None: x's)."""
+    if shape == x.shape and (dtype is None or dtype == x.dtype) and x.is_contiguous():
+        return _torch().empty_like(x)
+    return x.new_empty(shape, dtype=dtype)
 
 
 def _at(t):
@@ -625,17 +639,17 @@ def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = F
     ldg = 0 if gate is None else _token_rows(x, gate, "gate")
     h, fs, want = out, final_state, chunk_states is not None
     if h is None:
-        h = torch.empty(x.shape, dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
+        h = _empty(x, x.shape, out_dtype)
     else:
         _check_like(x, out_dtype if out_dtype is not None else h.dtype, x.shape, "out", h)
     if fs is not None:
         _check_like(x, torch.float32, (N,) + ch, "final_state", fs)
     elif output_final_state:
-        fs = torch.empty((N,) + ch, dtype=torch.float32, device=x.device)
+        fs = _empty(x, (N,) + ch, torch.float32)
     if want:
         shape = (-(-B * T // SCAN_CHUNK),) + ch
         if chunk_states is True:
-            chunk_states = torch.empty(shape, dtype=torch.float32, device=x.device)
+            chunk_states = _empty(x, shape, torch.float32)
         _check_like(x, torch.float32, shape, "chunk_states", chunk_states)
     _check_cuda(workspace)
     st = load_library().kda_scan_fwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(h), _at(fs),
@@ -678,12 +692,11 @@ def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=
     _check_like(x, torch.float32, (N,) + ch, "d_final_state", d_final_state)
     _check_like(x, torch.float32, (-(-B * T // SCAN_CHUNK),) + ch, "chunk_states", chunk_states)
     odt = out_dtype if out_dtype is not None else torch.float32
-    g = {k: torch.empty(x.shape, dtype=odt, device=x.device) for k in ("dx", "dlog_alpha")}
-    g["dgate"] = None if gate is None else torch.empty(x.shape, dtype=odt, device=x.device)
-    g["d_initial_state"] = torch.empty((N,) + ch, dtype=torch.float32, device=x.device) \
-        if want_d_initial_state else None
+    g = {k: _empty(x, x.shape, odt) for k in ("dx", "dlog_alpha")}
+    g["dgate"] = None if gate is None else _empty(x, x.shape, odt)
+    g["d_initial_state"] = _empty(x, (N,) + ch, torch.float32) if want_d_initial_state else None
     if workspace is None and chunk_states is None:
-        workspace = torch.empty(scan_bwd_workspace_size(B, T, D), dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, (scan_bwd_workspace_size(B, T, D),), torch.uint8)
     _check_cuda(workspace)
     st = load_library().kda_scan_bwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(d_h),
                                      _at(d_final_state), _at(chunk_states), _at(g["dx"]), _at(g["dlog_alpha"]),
@@ -722,11 +735,11 @@ def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False
     _check_slots(x, slots, "slots", Bd)
     h, want = out, step_states is not None
     if h is None:
-        h = torch.empty(shape, dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
+        h = _empty(x, shape, out_dtype)
     else:
         _check_like(x, out_dtype if out_dtype is not None else h.dtype, shape, "out", h)
     if step_states is True:
-        step_states = torch.empty(shape, dtype=torch.float32, device=x.device)
+        step_states = _empty(x, shape, torch.float32)
     _check_like(x, torch.float32, shape, "step_states", step_states)
     st = load_library().kda_scan_decode_steps(_at(state), _at(x), _at(log_alpha), _at(gate), _at(h), _at(slots), P, n,
                                               Bd, math.prod(ch), _dt(x), _dt(h), int(normalize), _at(step_states),
@@ -743,6 +756,16 @@ def scan_decode_step(state, x, log_alpha, *, gate=None, normalize: bool = False,
     h = scan_decode_steps(state, one(x), one(log_alpha), gate=one(gate), normalize=normalize, slots=slots,
                           out_dtype=out_dtype, out=one(out), stream=stream)
     return out if out is not None else h[0]
+
+
+@functools.lru_cache(maxsize=64)
+def gate_norm_bwd_workspace_size(rows: int) -> int:
+    """Workspace bytes of gate_norm_bwd with d_norm_weight."""
+    n = ctypes.c_size_t(0)
+    st = load_library().kda_gate_norm_bwd_workspace_size(rows, HEAD_DIM, ctypes.byref(n))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_gate_norm_bwd_workspace_size")
+    return n.value
 
 
 def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=None,
@@ -763,15 +786,11 @@ def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=N
     _check_like(o, o.dtype, o.shape, "d_y", d_y)
     _check_like(o, torch.float32, (HEAD_DIM,), "norm_weight", norm_weight)
     rows = o.numel() // HEAD_DIM
-    odt, dev = out_dtype if out_dtype is not None else torch.float32, o.device
-    r = dict(d_o=torch.empty(o.shape, dtype=odt, device=dev), d_gate=torch.empty(o.shape, dtype=odt, device=dev),
-             d_norm_weight=torch.empty(HEAD_DIM, dtype=torch.float32, device=dev) if want_d_norm_weight else None)
+    odt = out_dtype if out_dtype is not None else torch.float32
+    r = dict(d_o=_empty(o, o.shape, odt), d_gate=_empty(o, o.shape, odt),
+             d_norm_weight=_empty(o, (HEAD_DIM,), torch.float32) if want_d_norm_weight else None)
     if workspace is None and want_d_norm_weight:
-        n = ctypes.c_size_t(0)
-        st = load_library().kda_gate_norm_bwd_workspace_size(rows, HEAD_DIM, ctypes.byref(n))
-        if st != KDA_OK:
-            raise KdaError(st, "kda_gate_norm_bwd_workspace_size")
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        workspace = _empty(o, (gate_norm_bwd_workspace_size(rows),), torch.uint8)
     st = load_library().kda_gate_norm_bwd(_at(o), _at(g), _at(d_y), _at(norm_weight), eps, _at(r["d_o"]),
                                           _at(r["d_gate"]), _at(r["d_norm_weight"]), rows, HEAD_DIM, _dt(o),
                                           _dt(r["d_o"]), _at(workspace),
@@ -843,7 +862,7 @@ def state_alloc(live, n: int, *, stream=None):
     if there is not None:
         with there:
             return state_alloc(live, n)
-    slots = torch.empty(n, dtype=torch.int32, device=live.device)
+    slots = _empty(live, (n,), torch.int32)
     st = load_library().kda_state_alloc(_at(live), live.numel(), _at(slots), n, _here(live.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_state_alloc")
@@ -875,8 +894,8 @@ def state_compact(live, *, stream=None):
         with there:
             return state_compact(live)
     P = live.numel()
-    r = {k: torch.empty(P, dtype=torch.int32, device=live.device) for k in ("dst_slots", "src_slots", "new_slots")}
-    r["n_live"] = torch.empty(1, dtype=torch.int32, device=live.device)
+    r = {k: _empty(live, (P,), torch.int32) for k in ("dst_slots", "src_slots", "new_slots")}
+    r["n_live"] = _empty(live, (1,), torch.int32)
     st = load_library().kda_state_compact(_at(live), P, _at(r["dst_slots"]), _at(r["src_slots"]), _at(r["new_slots"]),
                                           _at(r["n_live"]), _here(live.get_device()))
     if st != KDA_OK:
