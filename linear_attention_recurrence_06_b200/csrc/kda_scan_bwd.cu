@@ -22,9 +22,10 @@ struct ScanBwd {
     static constexpr int ROWS = NT * ScanGeo<BF16>::ROWB;                    // a warp's rows of one tensor
     static constexpr int STAGE = N_IN * ROWS;                                // [warps][2] stages
     static constexpr int OFF_AB = SC_WARPS * 2 * STAGE;                      // as in the forward
-    static constexpr int OFF_BAR = OFF_AB + 2 * SC_WARPS * 512;
-    static constexpr int OFF_EX = OFF_BAR + (4 * SC_WARPS + 4 * SC_MAX_CLUSTER) * 8;
-    static constexpr int smem(int cluster) { return OFF_EX + 4 * cluster * 512; }
+    static constexpr int OFF_BASE = OFF_AB + 2 * SC_WARPS * 512;             // [2][32] what a tile starts from
+    static constexpr int OFF_BAR = OFF_BASE + 2 * 256;                       // full[warps][2], given[warps][2], based[2]
+    static constexpr int OFF_EX = OFF_BAR + (4 * SC_WARPS + 2) * 8;          // [4][cluster][32] the CTAs' pieces, sent[4][cluster]
+    static constexpr int smem(int cluster) { return OFF_EX + 4 * cluster * (512 + 8); }
 };
 
 template <bool BF16, bool GATE, bool NORM>
@@ -41,15 +42,18 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + K::OFF_BAR);
     uint64_t* const full = bars + 2 * warp;                    // this warp's loads
     uint64_t* const given = bars + 2 * SC_WARPS + 2 * warp;    // this warp's piece
-    uint64_t* const sent = bars + 4 * SC_WARPS;                // the cluster's pieces, [4][cluster]
-    float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);
+    uint64_t* const based = bars + 4 * SC_WARPS;               // the gradient from behind the CTA's tile
+    float2* const base = reinterpret_cast<float2*>(smem + K::OFF_BASE);
+    float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);  // the cluster's pieces, [4][cluster][32]
+    uint64_t* const sent = reinterpret_cast<uint64_t*>(smem + K::OFF_EX + 4 * cluster * 512);
     uint8_t* const stages = smem + warp * 2 * K::STAGE;
     const bool even = (D & 1) == 0, tma = width == 16;
     bool failed = false;
 
     if (tma && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4 * SC_WARPS + 4 * cluster; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 4 * SC_WARPS + 2; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 4 * cluster; ++i) mbar_init(&sent[i], 1);
         fence_mbar_init();
         if (cluster > 1)
             for (int i = 0; i < 4 * cluster; ++i) mbar_arrive_expect_tx(&sent[i], 512);
@@ -107,7 +111,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             if (a.d_final && n >= 0) c_end = load2(a.d_final, n, D, ch);
         }
         if (tma) {
-            failed = failed || !mbar_wait(full + (s & 1), phase, a.status);
+            failed = failed || !scan_wait<false>(full + (s & 1), phase, a.status);
         } else {
             cp_wait<1>();
             __syncwarp();
@@ -185,7 +189,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         // the pieces of the warps with later tokens; its own joined to them goes on
         float4 before = make_float4(-0.f, -0.f, 0.f, 0.f);
         if (warp > 0) {
-            failed = failed || !mbar_wait(given - 2 + (s & 1), phase, a.status);
+            failed = failed || !scan_wait<false>(given - 2 + (s & 1), phase, a.status);
             before = ab[(warp - 1) * 32 + lane];
             piece = scan_join2(before, piece);
         }
@@ -204,15 +208,27 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 if (lane == 0) mbar_arrive(sent + slot);
             }
         }
-        for (int k = 0; k < cluster; ++k) {
-            const bool last = rank + k < cluster;
-            const int r = last ? rank + k : rank + k - cluster, q = last ? s - 1 : s, slot = (q & 3) * cluster + r;
-            if (q < 0) continue;
-            const uint32_t ph = (q >> 2) & 1;
-            failed = failed || !(cluster > 1 ? mbar_wait_peers(sent + slot, ph, a.status) : mbar_wait(sent + slot, ph, a.status));
-            if (cluster > 1 && warp == 0 && lane == 0) mbar_arrive_expect_tx(sent + slot, 512);  // for step q + 4
-            const float4 v = ex[slot * 32 + lane];
-            carry = scan_fold2(v, carry, scan_is_cut(v));
+        if (warp == 0) {
+            for (int k = 0; k < cluster; ++k) {
+                const bool last = rank + k < cluster;
+                const int r = last ? rank + k : rank + k - cluster, q = last ? s - 1 : s, slot = (q & 3) * cluster + r;
+                if (q < 0) continue;
+                const uint32_t ph = (q >> 2) & 1;
+                if (cluster > 1) {
+                    failed = failed || !scan_wait<true>(sent + slot, ph, a.status);
+                    if (lane == 0) mbar_arrive_expect_tx(sent + slot, 512);  // for step q + 4
+                } else {
+                    failed = failed || !scan_wait<false>(sent + slot, ph, a.status);
+                }
+                const float4 v = ex[slot * 32 + lane];
+                carry = scan_fold2(v, carry, scan_is_cut(v));
+            }
+            base[(s & 1) * 32 + lane] = carry;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(based + (s & 1));
+        } else {
+            failed = failed || !scan_wait<false>(based + (s & 1), phase, a.status);
+            carry = base[(s & 1) * 32 + lane];
         }
         float2 mine = warp > 0 ? scan_fold2(before, carry, scan_is_cut(before)) : carry;
         if (ends_here) mine = c_end;

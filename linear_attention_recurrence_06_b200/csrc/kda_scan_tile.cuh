@@ -7,12 +7,13 @@
 // piece of the recurrence is affine in the state before it, h -> A h + B with
 // A = e^{sum l}: a warp runs its tokens from zero, joins its piece (A, B) to those of
 // the warps before it and hands the result to the next warp; the last warp sends
-// the tile's piece to all CTAs of the cluster, which take neighbouring tiles.  Every
-// warp folds the pieces of all earlier tiles over a copy of its own of the carried
-// state and finishes its tokens in registers.  Pieces are always joined from left
-// to right: the result does not depend on timing.  Warps meet only at those
-// hand-overs (mbarriers); loads, too, are a warp's own, so that warps of
-// earlier tokens can be most of a step ahead of those that wait for them.
+// the tile's piece to all CTAs of the cluster, which take neighbouring tiles.  The
+// first warp folds the pieces of all earlier tiles over the carried state and gives
+// the others the state before the tile; each finishes its tokens in registers.
+// Pieces are always joined from left to right: the result does not depend on
+// timing.  Warps meet only at those hand-overs (mbarriers); loads, too, are a
+// warp's own, so that warps of earlier tokens can be most of a step ahead of those
+// that wait for them.
 // Why this split: the channels of one sequence alone (32 x 64 lanes for 4096) cannot
 // keep enough loads in flight, time has to be split; a cluster does that in one
 // pass over the data, without flags in global memory and without a second launch.
@@ -330,25 +331,40 @@ KDA_DEV ScanSeen scan_see(const ScanArgs& a, const ScanSpan& sp, int s, int tw, 
 // ---- clusters
 KDA_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 KDA_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Waits like mbar_wait, for what other CTAs of the cluster have written.
-KDA_DEV bool mbar_wait_peers(uint64_t* bar, uint32_t parity, uint32_t* status) {
-    unsigned long long t0 = 0;
-    while (true) {
-        uint32_t ok;
+// Waits like mbar_wait; PEERS: for what other CTAs of the cluster have written.  The first look is in
+// line, the rest out of it.
+template <bool PEERS>
+KDA_DEV bool scan_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (PEERS)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
-            : "memory");
-        if (ok) return true;
-        if (t0 == 0) t0 = globaltimer_ns();
-        else if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
+template <bool PEERS>
+__device__ __noinline__ bool scan_wait_long(uint32_t bar, uint32_t parity, uint32_t* status) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!scan_try<PEERS>(bar, parity)) {
+        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
             if (status) atomicOr(status, DEV_ERR_TIMEOUT);
             return false;
         }
     }
+    return true;
+}
+template <bool PEERS>
+KDA_DEV bool scan_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    const uint32_t b = smem_u32(bar);
+    return scan_try<PEERS>(b, parity) || scan_wait_long<PEERS>(b, parity, status);
 }
 // 16 bytes into a CTA's shared memory, counted on its barrier
 KDA_DEV void st_async16(uint32_t addr, float4 v, uint32_t bar) {
