@@ -108,10 +108,20 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
 
     ScanSeen at;
     at.calm = 0;
+    bool plain = false;
+    float2 h0 = f2(0.f);     // where a sequence starts with this warp's first token: its initial state
     float2 carry = f2(0.f);  // the state before this CTA's tile
     for (int s = 0; s < n_steps; ++s, tw += by) {
         float4* const ab = reinterpret_cast<float4*>(smem + K::OFF_AB) + (s & 1) * (SC_WARPS * 32);
-        if (s >= at.calm) at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
+        if (s >= at.calm) {
+            at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
+            // whole rows, and sequences meet at most before the first token and behind the last
+            plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
+            if (at.starts & 1) {
+                const int n = at.seq_start(0);
+                h0 = a.init ? load2(a.init, n, D, ch) : f2(0.f);
+            }
+        }
         const uint32_t phase = (s >> 1) & 1;
         if (tma) {
             failed = failed || !scan_wait<false>(full + (s & 1), phase, a.status);
@@ -123,18 +133,11 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
 
         // the warp's tokens from zero: states h, products of the decays A
         float2 hs[NT], as[NT], sum = f2(0.f);
-        // whole rows, and sequences meet at most before the first token and behind the last
-        const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
-        float2 h0 = f2(0.f);
-        if (at.starts & 1) {
-            const int n = at.seq_start(0);
-            if (a.init) h0 = load2(a.init, n, D, ch);
-        }
         auto first_run = [&](auto edge) {
             constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                float2 d = scan_depth2(tile_at<BF16>(st, i, lane)), u = tile_at<BF16>(st + K::ROWS, i, lane);
+                float2 d = depth_at<BF16>(st, i, lane), u = tile_at<BF16>(st + K::ROWS, i, lane);
                 const float2 g = GATE ? tile_at<BF16>(st + 2 * K::ROWS, i, lane) : f2(0.f);
                 const bool own = !EDGE || (at.own >> i & 1);
                 if (!own) d = f2(0.f);
@@ -144,14 +147,14 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 sum = __fadd2_rn(sum, d);
                 if (i == 0) {
                     hs[0] = u;
-                    as[0] = __fadd2_rn(a2.e, a2.lo);
+                    as[0] = a2.a;
                 } else {
-                    hs[i] = scan_step2(a2.e, a2.lo, hs[i - 1], u);
-                    as[i] = __ffma2_rn(a2.lo, as[i - 1], __fmul2_rn(a2.e, as[i - 1]));
+                    hs[i] = __ffma2_rn(a2.a, hs[i - 1], u);
+                    as[i] = __fmul2_rn(a2.a, as[i - 1]);
                 }
                 if (EDGE && i > 0 && (at.starts >> i & 1)) {
                     const int n = at.seq_start(i);
-                    hs[i] = scan_step2(a2.e, a2.lo, a.init ? load2(a.init, n, D, ch) : f2(0.f), u);
+                    hs[i] = __ffma2_rn(a2.a, a.init ? load2(a.init, n, D, ch) : f2(0.f), u);
                 }
             }
         };

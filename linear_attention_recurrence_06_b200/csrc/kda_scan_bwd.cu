@@ -130,7 +130,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 float2 x = tile_at<BF16>(st + K::ROWS, i, lane), d = scan_depth2(la);
                 if (!own) d = x = f2(0.f);
                 const ScanDecay2 a2 = scan_decay2(d);
-                const float2 A = __ffma2_rn(a2.m, f2(-1.f), f2(1.f));
+                const float2 A = a2.a;
                 float2 sg = f2(1.f), w = f2(1.f), r = f2(0.f);
                 if (GATE) {
                     const float2 g = tile_at<BF16>(st + 3 * K::ROWS, i, lane), y = __fmul2_rn(g, f2(-LOG2E));

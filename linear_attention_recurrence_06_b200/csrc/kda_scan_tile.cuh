@@ -37,34 +37,46 @@ struct ScanGeo {
 KDA_DEV float2 f2(float x, float y) { return make_float2(x, y); }
 KDA_DEV float2 f2(float x) { return make_float2(x, x); }
 
-// The tiled kernels keep a decay as e + lo: e = e^l as the hardware approximates it, lo what is missing
-// to 1 - m, m = 1 - e^l by its Taylor polynomial where l > -1/4 (and 1 - e, so that lo = 0, elsewhere).  A
-// step is then two fused products for two channels at once, without a choice, and keeps slow
-// and fast decays as scan_step does.  `d` = -l >= 0.
+// Decays of two channels, `d` = -l >= 0:  a = e^-d and m = 1 - a.  m is its Taylor polynomial to d^5 below
+// 1/8 (the next term is below 2^-24 of m there), where a = 1 - m; above it a is the hardware's e^-d,
+// and m what that leaves of 1.  A warp's tokens are stepped with a as it is: its rounding does
+// not add up beyond them, for what is handed on goes by the sum of the d (scan_piece).
+constexpr float SCAN_NEAR = 0.125f;
 struct ScanDecay2 {
-    float2 e, lo, m;
+    float2 a, m;
 };
 KDA_DEV ScanDecay2 scan_decay2(float2 d) {
     ScanDecay2 r;
-    float2 t = __ffma2_rn(d, f2(-1.f / 720.f), f2(1.f / 120.f));
-    t = __ffma2_rn(t, d, f2(-1.f / 24.f));
+    float2 t = __ffma2_rn(d, f2(1.f / 120.f), f2(-1.f / 24.f));
     t = __ffma2_rn(t, d, f2(1.f / 6.f));
     t = __ffma2_rn(t, d, f2(-0.5f));
-    const float2 slow = __ffma2_rn(__fmul2_rn(t, d), d, d);
+    const float2 near = __ffma2_rn(__fmul2_rn(t, d), d, d);
     const float2 x = __fmul2_rn(d, f2(-LOG2E));
-    r.e = f2(ex2_ftz(x.x), ex2_ftz(x.y));
-    const float2 m1 = __ffma2_rn(r.e, f2(-1.f), f2(1.f));
-    r.m = f2(d.x < -SCAN_SLOW ? slow.x : m1.x, d.y < -SCAN_SLOW ? slow.y : m1.y);
-    r.lo = __ffma2_rn(r.m, f2(-1.f), m1);
+    const float2 e = f2(ex2_ftz(x.x), ex2_ftz(x.y));
+    const float2 m1 = __ffma2_rn(e, f2(-1.f), f2(1.f)), a1 = __ffma2_rn(near, f2(-1.f), f2(1.f));
+    const bool nx = d.x < SCAN_NEAR, ny = d.y < SCAN_NEAR;
+    r.m = f2(nx ? near.x : m1.x, ny ? near.y : m1.y);
+    r.a = f2(nx ? a1.x : e.x, ny ? a1.y : e.y);
     return r;
 }
-KDA_DEV float2 scan_step2(float2 e, float2 lo, float2 h, float2 u) { return __ffma2_rn(lo, h, __ffma2_rn(e, h, u)); }
 // -l of two channels: max(-log_alpha, 0), NaN kept
 KDA_DEV float2 scan_depth2(float2 log_alpha) {
     float2 r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(-log_alpha.x), "f"(0.f));
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(-log_alpha.y), "f"(0.f));
     return r;
+}
+KDA_DEV float2 unpack2(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+// The same from a tile's row: two bf16 are clamped at once.
+template <bool BF16>
+KDA_DEV float2 depth_at(const uint8_t* tile, int row, int lane) {
+    if constexpr (BF16) {
+        uint32_t w = *reinterpret_cast<const uint32_t*>(tile + row * (SC_CH * 2) + lane * 4) ^ 0x80008000u;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(w), "r"(0u));
+        return unpack2(w);
+    } else {
+        return scan_depth2(*reinterpret_cast<const float2*>(tile + row * (SC_CH * 4) + lane * 8));
+    }
 }
 
 // w s of two channels.  With both factors w s = sqrt(n) / q = n rsqrt(n q^2), n = 1 - a^2, q = 1 + e^-gate:
@@ -95,7 +107,7 @@ KDA_DEV float2 scan_step2(float2 p, float2 h, float2 u) {
 }
 KDA_DEV float4 scan_piece(bool cut, float2 depth, float2 b) {
     const ScanDecay2 d = scan_decay2(depth);
-    const float2 p = f2(depth.x < -SCAN_SLOW ? -d.m.x : d.e.x, depth.y < -SCAN_SLOW ? -d.m.y : d.e.y);
+    const float2 p = f2(depth.x < SCAN_NEAR ? -d.m.x : d.a.x, depth.y < SCAN_NEAR ? -d.m.y : d.a.y);
     return make_float4(cut ? SC_CUT : p.x, cut ? SC_CUT : p.y, b.x, b.y);
 }
 KDA_DEV float2 scan_fold2(float4 v, float2 h) { return scan_step2(f2(v.x, v.y), h, f2(v.z, v.w)); }
@@ -158,8 +170,7 @@ __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t l
 template <bool BF16>
 KDA_DEV float2 tile_at(const uint8_t* tile, int row, int lane) {
     if constexpr (BF16) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + row * (SC_CH * 2) + lane * 4);
-        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        return unpack2(*reinterpret_cast<const uint32_t*>(tile + row * (SC_CH * 2) + lane * 4));
     } else {
         return *reinterpret_cast<const float2*>(tile + row * (SC_CH * 4) + lane * 8);
     }
@@ -187,7 +198,7 @@ template <bool BF16>
 __device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
     const size_t i = (size_t)t * ld + ch;
     const float2 d = scan_depth2(f2(ch < D ? ld_in<BF16>(log_alpha, i) : 0.f, ch + 1 < D ? ld_in<BF16>(log_alpha, i + 1) : 0.f));
-    return __ffma2_rn(scan_decay2(d).m, f2(-1.f), f2(1.f));
+    return scan_decay2(d).a;
 }
 KDA_DEV float2 load2(const float* base, size_t row, int D, int ch) {
     const size_t i = row * D + ch;
