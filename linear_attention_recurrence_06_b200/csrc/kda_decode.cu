@@ -265,16 +265,17 @@ decode_multi_kernel(float* __restrict__ state, const void* __restrict__ q, const
         // beta of step t0 + tid: kept in a register until the block's wait
         return tid < nb ? ld_in<IN_BF16>(beta, (size_t)(t0 + tid) * BH + bh) : 0.f;
     };
+    float beta_next = fetch_block(0);  // in flight with the state load
     size_t page = bh;  // of one head
     if constexpr (PAGED) {
         const int slot = slots[bh / H];
         if (!slot_in_range(slot, n_slots)) {
+            cp_async_wait_all();
             zero_row<OUT_BF16, 128>(o, step_states, n_steps, BH, bh, 64 * sl, 64);
             return;
         }
         page = (size_t)slot * H + bh % H;
     }
-    float beta_next = fetch_block(0);  // in flight with the state load
 
     float* S = state + page * D * D;
     float2 st[32];
