@@ -372,7 +372,8 @@ KDA_API kda_status kda_gate_norm(const void* o, const void* gate, const float* n
  * lie; they need element alignment only (16-byte aligned pointers with strides
  * of whole 16 bytes load fastest).  Here and below, cu_seqlens and vectors of
  * slots need 4-byte alignment, all other pointers 16-byte alignment.  D is any
- * positive size; B * T stays below 2^31 - 65536 tokens.
+ * size from 1 to 2^28; B * T is at most 2^31 - 65536 tokens.  What is not finite
+ * stays in its channel and sequence, where an infinite state may turn to NaN.
  *
  *   cu_seqlens   device int32 [n_seqs + 1], cu[0] = 0, non-decreasing,
  *                cu[n_seqs] <= T, or NULL for B sequences of T tokens.  Rows of

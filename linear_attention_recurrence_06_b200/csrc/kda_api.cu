@@ -405,7 +405,7 @@ kda_status scan_check(const kda::ScanArgs& a, kda_dtype in_dtype, kda_dtype out_
     } else {
         *n_seqs = a.B;
     }
-    if (a.T > kda::SCAN_MAX_TOKENS / a.B) return KDA_ERR_UNSUPPORTED;
+    if (a.T > kda::SCAN_MAX_TOKENS / a.B || a.D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;
     const void* in[] = {a.x, a.log_alpha, a.gate, a.d_h};
     for (const void* p : in)
         if (p && !element_aligned(p, in_dtype)) return KDA_ERR_MISALIGNED;
@@ -450,7 +450,7 @@ kda_status kda_scan_fwd(const void* x, const void* log_alpha, const void* gate, 
 
 kda_status kda_scan_bwd_workspace_size(int B, int64_t T, int D, size_t* bytes) {
     if (B <= 0 || T < 0 || D <= 0 || !bytes) return KDA_ERR_INVALID_ARG;
-    if (T > kda::SCAN_MAX_TOKENS / B) return KDA_ERR_UNSUPPORTED;
+    if (T > kda::SCAN_MAX_TOKENS / B || D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;
     const size_t chunks = (size_t)(((int64_t)B * T + KDA_SCAN_CHUNK - 1) / KDA_SCAN_CHUNK);
     *bytes = KDA_STATUS_BYTES + chunks * (size_t)D * sizeof(float);
     return KDA_OK;
@@ -497,7 +497,7 @@ kda_status kda_scan_decode_steps(float* state, const void* x, const void* log_al
         return KDA_ERR_INVALID_ARG;
     if (Bd == 0 || n_steps == 0) return KDA_OK;
     if (!state || !x || !log_alpha || !h || (!slots && n_slots < Bd)) return KDA_ERR_INVALID_ARG;
-    if (Bd > 65535) return KDA_ERR_UNSUPPORTED;  // grid y extent
+    if (Bd > 65535 || D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;  // grid y extent
     const void* ptrs[] = {state, x, log_alpha, gate, h, step_states};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;

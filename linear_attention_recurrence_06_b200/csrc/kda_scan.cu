@@ -72,7 +72,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     const bool even = (D & 1) == 0, tma = width == 16;
     bool failed = false;
 
-    if (tma && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
+    if (tma && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4 * SC_WARPS + 2; ++i) mbar_init(&bars[i], 1);
         for (int i = 0; i < 4 * cluster; ++i) mbar_init(&sent[i], 1);
@@ -268,7 +268,14 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     cp_wait<0>();
     if (failed && tma && lane == 0)  // loads still in flight
         for (int s = n_steps < 2 ? 0 : n_steps - 2; s < n_steps; ++s) mbar_wait(full + (s & 1), (s >> 1) & 1, nullptr);
-    if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may write to it
+    if (cluster > 1) {
+        // The last step's pieces of this and the later CTAs have not been looked at: they have to
+        // arrive before this CTA's memory goes, and no CTA leaves while another may write to it.
+        if (warp == 0 && n_steps > 0 && !failed)
+            for (int k = rank; k < cluster; ++k)
+                scan_wait<true>(sent + ((n_steps - 1) & 3) * cluster + k, ((n_steps - 1) >> 2) & 1, a.status);
+        cluster_sync_all();
+    }
     // sequences without tokens
     if (a.final_state && rank == 0) {
         for (int n = sp.n0 + warp; n < sp.n1; n += SC_WARPS) {

@@ -8,6 +8,7 @@ namespace kda {
 
 constexpr int SCAN_CHUNK = 8;   // tokens between two rows of chunk_states
 constexpr int64_t SCAN_MAX_TOKENS = (int64_t(1) << 31) - 65536;  // B * T: tokens are counted in 32 bits
+constexpr int SCAN_MAX_D = 1 << 28;
 
 struct ScanArgs {
     const void *x, *log_alpha, *gate;

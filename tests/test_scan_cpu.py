@@ -87,7 +87,7 @@ def test_scan_fwd_refusals(lib):
     assert f(cu=FAKE, N=2) == -1             # packed sequences: B = 1
     assert f(cu=FAKE, B=1, N=0) == -1
     assert f(cu=FAKE, B=1, N=1, T=1 << 31) == -2
-    assert f(T=1 << 41) == -2
+    assert f(T=1 << 41) == -2 and f(B=1 << 20, T=2048) == -2 and f(D=(1 << 28) + 1) == -2
     assert f(x=FAKE + 1) == -3 and f(la=FAKE + 2, idt=0) == -3
     assert f(s0=FAKE + 8) == -3 and f(h=FAKE + 2) == -3 and f(fs=FAKE + 4) == -3 and f(cs=FAKE + 4) == -3
     assert f(cu=FAKE + 2, B=1, N=1) == -3 and f(ws=FAKE, wsb=255) == -4 and f(ws=FAKE + 8, wsb=256) == -3
