@@ -228,7 +228,12 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const bool own = at.own >> i & 1, from_start = at.starts & ((1u << i) - 2u) & ((1u << i) - 1u);
                 float2 h = mine;
                 if (i > 0) h = from_start ? hs[i - 1] : __ffma2_rn(as[i - 1], mine, hs[i - 1]);
-                if (own) store2(a.chunk_states, false, (tw + i) / SCAN_CHUNK, D, ch, h);
+                if (own && even) {
+                    if (ch < D)
+                        *reinterpret_cast<float2*>(a.chunk_states + (size_t)((tw + i) / SCAN_CHUNK) * D + ch) = h;
+                } else if (own) {
+                    store2(a.chunk_states, false, (tw + i) / SCAN_CHUNK, D, ch, h);
+                }
             }
         }
         // the same tokens from that state

@@ -39,23 +39,19 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
     return cudaSuccess;
 }
 
-// Splits and cluster.  Two CTAs fit on an SM with clusters of up to 4, one with more.  Splitting the
-// batch costs nothing, splitting time costs an exchange per tile, so time is only split where
-// the batch leaves SMs without work.  Packed sequences may be one long one: they are split
-// only where 8 CTAs in time would not do.
+// Splits and cluster, for `per_sm` CTAs on an SM with clusters of up to 4 (one with more).  Splitting
+// the batch costs nothing, splitting time costs an exchange per tile, so time is only split
+// where the batch leaves SMs without work.  Of packed sequences one may be long: time first,
+// by 4, then the sequences.
 struct ScanGrid {
     int groups, splits, cluster;
 };
-inline ScanGrid scan_grid(const ScanArgs& a, int sms, int tile) {
+inline ScanGrid scan_grid(const ScanArgs& a, int sms, int per_sm, int tile) {
     ScanGrid g{(a.D + SC_CH - 1) / SC_CH, 1, 1};
     const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
     auto clamp = [](int64_t v, int64_t hi) { return (int)(v < 1 ? 1 : (v > hi ? hi : v)); };
-    const int want = clamp(2 * sms / g.groups, 65535);
-    if (!a.cu) {
-        g.splits = clamp(want, a.B);
-    } else if (want > SC_MAX_CLUSTER) {
-        g.splits = clamp(want / SC_MAX_CLUSTER, a.n_seqs);
-    }
+    const int want = clamp(per_sm * sms / g.groups, 65535);
+    g.splits = a.cu ? clamp(want / 4, a.n_seqs) : clamp(want, a.B);
     const int64_t tiles = (tokens / g.splits + tile) / tile;  // one at least
     const bool few = (int64_t)g.groups * g.splits * SC_MAX_CLUSTER <= sms;
     g.cluster = clamp(clamp(want / g.splits, few ? SC_MAX_CLUSTER : 4), tiles);
@@ -76,7 +72,7 @@ cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const Sca
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const ScanGrid g = scan_grid(a, sms, tile);
+    const ScanGrid g = scan_grid(a, sms, 2 * (smem(4) + 1024) <= 228 * 1024 ? 2 : 1, tile);
     if ((int64_t)g.groups * g.cluster > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(g.groups * g.cluster), (unsigned)g.splits);
