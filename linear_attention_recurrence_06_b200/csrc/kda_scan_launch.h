@@ -39,53 +39,57 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
     return cudaSuccess;
 }
 
-// Splits and cluster, for `per_sm` CTAs on an SM with clusters of up to 4 (one with more).  Splitting
-// the batch costs nothing, splitting time costs an exchange per tile, so time is only split
-// where the batch leaves SMs without work.  Of packed sequences one may be long: time first,
-// by 4, then the sequences.
-struct ScanGrid {
-    int groups, splits, cluster;
-};
-inline ScanGrid scan_grid(const ScanArgs& a, int sms, int per_sm, int tile) {
-    ScanGrid g{(a.D + SC_CH - 1) / SC_CH, 1, 1};
-    const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
-    auto clamp = [](int64_t v, int64_t hi) { return (int)(v < 1 ? 1 : (v > hi ? hi : v)); };
-    const int want = clamp(per_sm * sms / g.groups, 65535);
-    g.splits = a.cu ? clamp(want / 4, a.n_seqs) : clamp(want, a.B);
-    const int64_t tiles = (tokens / g.splits + tile) / tile;  // one at least
-    const bool few = (int64_t)g.groups * g.splits * SC_MAX_CLUSTER <= sms;
-    g.cluster = clamp(clamp(want / g.splits, few ? SC_MAX_CLUSTER : 4), tiles);
-    return g;
-}
-
+// Splits of the batch and cluster.  Splitting the batch costs nothing, splitting time costs an
+// exchange per tile, so time is only split where the batch leaves SMs without work; of packed
+// sequences one may be long, so there time comes first, by 4.  The cluster is then the
+// largest of which all run at once: a second wave doubles the time (16 clusters of 8, of
+// which not all find room, took 67 us for 8192 x 1024 values; as clusters of 7, 45 us).
 template <auto KERNEL>
 cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const ScanMaps& maps, int width,
                         cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};  // devices on which this kernel may use its shared memory
+    static std::atomic<uint64_t> ready{0};           // devices on which this kernel may use its shared memory
+    static std::atomic<int> active[64][SC_MAX_CLUSTER + 1];  // clusters of a size that run at once, + 1
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
         if ((e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(SC_MAX_CLUSTER))) !=
             cudaSuccess)
             return e;
-        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+        ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const ScanGrid g = scan_grid(a, sms, 2 * (smem(4) + 1024) <= 228 * 1024 ? 2 : 1, tile);
-    if ((int64_t)g.groups * g.cluster > INT32_MAX) return cudaErrorInvalidValue;
+
+    auto clamp = [](int64_t v, int64_t hi) { return (int)(v < 1 ? 1 : (v > hi ? hi : v)); };
+    const int groups = (a.D + SC_CH - 1) / SC_CH;
+    const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
+    const int per_sm = 2 * (smem(4) + 1024) <= 228 * 1024 ? 2 : 1;
+    const int want = clamp(per_sm * sms / groups, 65535);
+    const int splits = a.cu ? clamp(want / 4, a.n_seqs) : clamp(want, a.B);
+    int cluster = clamp(clamp(want / splits, SC_MAX_CLUSTER), (tokens / splits + tile) / tile);
+
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(g.groups * g.cluster), (unsigned)g.splits);
     cfg.blockDim = dim3(SC_THREADS);
-    cfg.dynamicSmemBytes = smem(g.cluster);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = g.cluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = g.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, KERNEL, a, maps, g.cluster, width);
+    for (;; --cluster) {
+        cfg.gridDim = dim3((unsigned)(groups * cluster), (unsigned)splits);
+        cfg.dynamicSmemBytes = smem(cluster);
+        cfg.numAttrs = cluster > 1 ? 1 : 0;
+        at.val.clusterDim.x = cluster;
+        if (cluster == 1) break;
+        int n = active[dev][cluster].load(std::memory_order_relaxed) - 1;
+        if (n < 0) {
+            if ((e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg)) != cudaSuccess) return e;
+            active[dev][cluster].store(n + 1, std::memory_order_relaxed);
+        }
+        if ((int64_t)groups * splits <= n) break;
+    }
+    return cudaLaunchKernelEx(&cfg, KERNEL, a, maps, cluster, width);
 }
 
 }  // namespace kda
