@@ -32,7 +32,8 @@ struct ScanArgs {
 };
 
 struct ScanMaps {
-    CUtensorMap m[4];  // log_alpha, x, gate, d_h
+    CUtensorMap m[4];    // log_alpha, x, then gate (forward) or d_h, gate (backward)
+    CUtensorMap states;  // backward: chunk_states
 };
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);

@@ -20,7 +20,7 @@ struct ScanBwd {
     static constexpr int NT = SCAN_CHUNK;                                    // tokens of a warp
     static constexpr int N_IN = GATE ? 4 : 3;
     static constexpr int ROWS = NT * ScanGeo<BF16>::ROWB;                    // a warp's rows of one tensor
-    static constexpr int STAGE = N_IN * ROWS;                                // [warps][2] stages
+    static constexpr int STAGE = N_IN * ROWS + SC_CH * 4;                    // [warps][2] stages: and the state before them
     static constexpr int OFF_AB = SC_WARPS * 2 * STAGE;                      // as in the forward
     static constexpr int OFF_BASE = OFF_AB + 2 * SC_WARPS * 512;             // [2][32] what a tile starts from
     static constexpr int OFF_BAR = OFF_BASE + 2 * 256;                       // full[warps][2], given[warps][2], based[2]
@@ -50,7 +50,8 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     const bool even = (D & 1) == 0, tma = width == 16;
     bool failed = false;
 
-    if (tma && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
+    if (tma && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x <= 32 + K::N_IN)
+        prefetch_tmap(threadIdx.x < 32 + K::N_IN ? &maps.m[threadIdx.x - 32] : &maps.states);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4 * SC_WARPS + 2; ++i) mbar_init(&bars[i], 1);
         for (int i = 0; i < 4 * cluster; ++i) mbar_init(&sent[i], 1);
@@ -71,6 +72,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 mbar_arrive_expect_tx(b, K::STAGE);
 #pragma unroll
                 for (int i = 0; i < K::N_IN; ++i) tma_load_2d(st + i * K::ROWS, &maps.m[i], ch0, y, b);
+                tma_load_2d(st + K::N_IN * K::ROWS, &maps.states, ch0, y / SCAN_CHUNK, b);
             }
         } else {
             if (s < n_steps) {
@@ -78,16 +80,14 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 load_rows<BF16, NT>(st + K::ROWS, a.x, a.ld_x, t, sp.t0, sp.t1, ch0, D, width, lane);
                 load_rows<BF16, NT>(st + 2 * K::ROWS, a.d_h, a.ld_dh, t, sp.t0, sp.t1, ch0, D, width, lane);
                 if (GATE) load_rows<BF16, NT>(st + 3 * K::ROWS, a.gate, a.ld_g, t, sp.t0, sp.t1, ch0, D, width, lane);
+                const int c = t < sp.t0 || t >= sp.t1 ? -1 : t / SCAN_CHUNK;
+                load_rows<false, 1>(st + K::N_IN * K::ROWS, a.chunk_states, D, c, 0, INT32_MAX, ch0, D, 4, lane);
             }
             cp_commit();
         }
     };
-    auto kept_state = [&](int t) {  // the state before token t
-        return t >= sp.t0 && t < sp.t1 ? load2(a.chunk_states, t / SCAN_CHUNK, D, ch) : f2(0.f);
-    };
     load(0, tw);
     load(1, tw + by);
-    float2 kept = kept_state(tw);
     if (cluster > 1) cluster_sync_all();  // every CTA's barriers are set up before another writes to them
 
     ScanSeen at;
@@ -99,12 +99,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         const uint32_t phase = (s >> 1) & 1;
         // whole rows, and sequences meet at most before the first token and behind the last
         const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
-        float2 h = kept, c_end = f2(0.f);
-        kept = kept_state(tw + by);
-        if (at.starts & 1) {
-            const int n = at.seq_start(0);
-            h = a.init ? load2(a.init, n, D, ch) : f2(0.f);
-        }
+        float2 c_end = f2(0.f);
         const bool ends_here = at.ends >> (NT - 1) & 1;
         if (ends_here) {
             const int n = at.seq_end(NT - 1);
@@ -117,6 +112,11 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             __syncwarp();
         }
         const uint8_t* const st = stages + (s & 1) * K::STAGE;
+        float2 h = tile_at<false>(st + K::N_IN * K::ROWS, 0, lane);
+        if (at.starts & 1) {
+            const int n = at.seq_start(0);
+            h = a.init ? load2(a.init, n, D, ch) : f2(0.f);
+        }
 
         // forwards: the factors of each token; then back from zero: G, and the products of the decays
         // behind each token
@@ -322,6 +322,10 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, bool own_states, cudaStream_t str
     ScanMaps maps;
     int width = 0;
     if ((e = scan_maps(a, in, ld, a.gate ? 4 : 3, SCAN_CHUNK, &maps, &width)) != cudaSuccess) return e;
+    const int64_t chunks = ((a.cu ? a.T : (int64_t)a.B * a.T) + SCAN_CHUNK - 1) / SCAN_CHUNK;
+    if (width == 16 && a.D % 4 != 0) width = 4;
+    if (width == 16 && chunks > 0 && !make_scan_map(&maps.states, a.chunk_states, chunks, a.D, a.D, 1, false))
+        return cudaErrorInvalidValue;
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
         if (a.in_bf16)
             e = scan_launch<scan_bwd_kernel<true, G, W>>(ScanBwd<true, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width,
