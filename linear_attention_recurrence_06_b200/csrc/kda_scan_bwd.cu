@@ -274,9 +274,15 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const bool from_end = at.ends & (((1u << (NT - 1)) - 1u) & ~((1u << i) - 1u));
                 const float2 G = from_end ? gs[i] : __ffma2_rn(as[i], mine, gs[i]);
                 if (!(at.own >> i & 1)) continue;
-                store2(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
-                store2(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
-                if (GATE) store2(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
+                if (!BF16 && even) {  // in line where the registers allow it
+                    store2_even(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
+                    store2_even(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
+                    if (GATE) store2_even(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
+                } else {
+                    store2(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
+                    store2(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
+                    if (GATE) store2(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
+                }
                 if ((at.starts >> i & 1) && a.d_init) {
                     const int n = at.seq_start(i);
                     store2(a.d_init, false, n, D, ch, __fmul2_rn(tile_decay<BF16>(a.log_alpha, a.ld_l, tw + i, D, ch), G));

@@ -193,6 +193,13 @@ static __device__ __noinline__ void store2(void* base, bool bf16, size_t row, in
         else static_cast<float*>(base)[i + 1] = v.y;
     }
 }
+// The same in line for even D.
+KDA_DEV void store2_even(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
+    if (ch >= D) return;
+    const size_t i = row * D + ch;
+    if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + i) = pack_bf16x2(v.x, v.y);
+    else *reinterpret_cast<float2*>(static_cast<float*>(base) + i) = v;
+}
 // The decays of a token's channels ch, ch + 1 from global memory (for the few that begin a sequence).
 template <bool BF16>
 __device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
