@@ -57,8 +57,9 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     constexpr int NT = K::NT, TILE = SC_WARPS * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = blockIdx.x % cluster, ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
-    const ScanSpan sp = scan_span(a, blockIdx.y, gridDim.y, lane);
+    const int ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
+    int rank = blockIdx.x % cluster;
+    const ScanSpan sp = scan_span(a, blockIdx.y, gridDim.y, TILE, &cluster, &rank, lane);  // changes cluster and rank, too
     const int tile0 = sp.t0 / TILE, n_tiles = sp.t1 > sp.t0 ? (sp.t1 + TILE - 1) / TILE - tile0 : 0;
     const int n_steps = (n_tiles + cluster - 1) / cluster;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + K::OFF_BAR);
@@ -271,8 +272,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         }
     }
     cp_wait<0>();
-    if (failed && tma && lane == 0)  // loads still in flight
-        for (int s = n_steps < 2 ? 0 : n_steps - 2; s < n_steps; ++s) mbar_wait(full + (s & 1), (s >> 1) & 1, nullptr);
+    if (failed && tma && lane == 0) scan_drain(full);
     if (cluster > 1) {
         // The last step's pieces of this and the later CTAs have not been looked at: they have to
         // arrive before this CTA's memory goes, and no CTA leaves while another may write to it.

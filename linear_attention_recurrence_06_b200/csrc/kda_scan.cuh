@@ -13,10 +13,8 @@ namespace kda {
 constexpr float SCAN_SLOW = -0.25f;
 
 struct ScanTerm {
-    float p;   // the decay, as above
-    float ws;  // w s: what x is multiplied with
-    float u;   // w s x
-    float s;   // sigmoid(gate), 1 without a gate
+    float p;  // the decay, as above
+    float u;  // w s x
 };
 
 // The hardware's approximations without their denormal handling (results below 2^-126 are 0).
@@ -67,26 +65,19 @@ KDA_DEV float scan_step(float p, float h, float u) {
 // 1 - a^2
 KDA_DEV float scan_one_minus_a2(float p) { return fmaf(-p, p, scan_slow(p) ? -2.f * p : 1.f); }
 
-constexpr float SCAN_TINY = 1e-37f;  // 1 - a^2 below this counts as 0
+constexpr float SCAN_TINY = 1e-37f;  // keeps sqrt(n) = n rsqrt(n), n = 1 - a^2, a number at n = 0
 
 template <bool GATE, bool NORM>
 KDA_DEV ScanTerm scan_term(float x, float log_alpha, float g) {
     ScanTerm r;
     r.p = scan_decay(scan_clamp(log_alpha));
-    r.s = GATE ? rcp_ftz(1.f + exp_ftz(-g)) : 1.f;
-    r.ws = r.s;
+    float ws = GATE ? rcp_ftz(1.f + exp_ftz(-g)) : 1.f;
     if (NORM) {
         const float n = scan_one_minus_a2(r.p);
-        r.ws *= n * rsqrt_ftz(fmaxf(n, SCAN_TINY));
+        ws *= n * rsqrt_ftz(fmaxf(n, SCAN_TINY));
     }
-    r.u = r.ws * x;
+    r.u = ws * x;
     return r;
-}
-
-// d u / d l = -a^2 s x / w, 0 where w is
-KDA_DEV float scan_du_dl(const ScanTerm& r) {
-    const float n = scan_one_minus_a2(r.p), a = scan_a(r.p);
-    return n < SCAN_TINY ? 0.f : -a * a * __fdividef(r.u, n);
 }
 
 // Tokens [first, end) of sequence n: cu (clamped into [0, T]) or n * T.

@@ -41,9 +41,16 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
 
 // Splits of the batch and cluster.  Splitting the batch costs nothing, splitting time costs an
 // exchange per tile, so time is only split where the batch leaves SMs without work; of packed
-// sequences one may be long, so there time comes first, by 4.  The cluster is then the
-// largest of which all run at once: a second wave doubles the time (16 clusters of 8, of
-// which not all find room, took 67 us for 8192 x 1024 values; as clusters of 7, 45 us).
+// sequences one may be long, so there time comes first, by up to 4, but not by more than
+// half of what the GPU takes (scan_span).  The cluster is then the largest of which all run at
+// once: a second wave doubles the time (16 clusters of 8, of which not all find room,
+// took 67 us for 8192 x 1024 values; as clusters of 7, 42 us).
+// Work that fills the GPU is cut finer, into up to 4 times as many splits, so that SMs which
+// have done their part find more (16 x 8192 x 4096: 813 -> 699 us, 6 x 4096 x 4096: 212 -> 167 us;
+// 125,841 tokens in 16 packed sequences x 4096, in 8 splits of 2 instead of 1 of 4: 1,042 -> 803 us),
+// as long as a CTA has 2,048 tokens, about 20 us: its start costs several (4,620 tokens x 1000 in
+// splits of 144: 38 us, of 288: 31 us).
+constexpr int64_t SC_PART_TOKENS = 2048;
 template <auto KERNEL>
 cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const ScanMaps& maps, int width,
                         cudaStream_t stream) {
@@ -66,8 +73,14 @@ cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const Sca
     const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
     const int per_sm = 2 * (smem(4) + 1024) <= 228 * 1024 ? 2 : 1;
     const int want = clamp(per_sm * sms / groups, 65535);
-    const int splits = a.cu ? clamp(want / 4, a.n_seqs) : clamp(want, a.B);
-    int cluster = clamp(clamp(want / splits, SC_MAX_CLUSTER), (tokens / splits + tile) / tile);
+    const int at_once = a.cu ? clamp(want / clamp(want / 2, 4), a.n_seqs) : clamp(want, a.B);
+    int cluster = clamp(clamp(want / at_once, SC_MAX_CLUSTER), (tokens / at_once + tile) / tile);
+    int splits = clamp(tokens / (SC_PART_TOKENS * cluster), a.cu ? a.n_seqs : a.B);
+    splits = splits < at_once ? at_once : clamp(splits, 4 * (int64_t)at_once);
+    if (!a.cu) {
+        const int each = (a.B + splits - 1) / splits;  // sequences of a split
+        splits = (a.B + each - 1) / each;
+    }
 
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(SC_THREADS);
@@ -87,7 +100,7 @@ cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const Sca
             if ((e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg)) != cudaSuccess) return e;
             active[dev][cluster].store(n + 1, std::memory_order_relaxed);
         }
-        if ((int64_t)groups * splits <= n) break;
+        if ((int64_t)groups * at_once <= n) break;
     }
     return cudaLaunchKernelEx(&cfg, KERNEL, a, maps, cluster, width);
 }

@@ -142,7 +142,6 @@ __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t l
                                        int width, int lane) {
     using Geo = ScanGeo<BF16>;
     constexpr int ES = Geo::ES;
-    uint8_t* const rows = dst;
     const uint8_t* const src = static_cast<const uint8_t*>(base);
     for (int i = 0; i < NT; ++i) {
         const int t = tw + i;
@@ -153,7 +152,7 @@ __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t l
                 const int ch = ch0 + (lane + 32 * k) * (4 / ES);
                 const int left = (D - ch) * ES, n = left < 0 ? 0 : (left > 4 ? 4 : left);
                 const bool in = row_in && n > 0;
-                cp_async4_zfill(smem_u32(rows + i * Geo::ROWB + (lane + 32 * k) * 4),
+                cp_async4_zfill(smem_u32(dst + i * Geo::ROWB + (lane + 32 * k) * 4),
                                 in ? src + ((size_t)t * ld + ch) * ES : src, in ? n : 0);
             }
         } else {
@@ -161,7 +160,7 @@ __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t l
             const int ch = ch0 + 2 * lane;
             const uint32_t lo = row_in && ch < D ? s[ch] : 0u;
             const uint32_t hi = row_in && ch + 1 < D ? s[ch + 1] : 0u;
-            *reinterpret_cast<uint32_t*>(rows + i * Geo::ROWB + lane * 4) = lo | hi << 16;
+            *reinterpret_cast<uint32_t*>(dst + i * Geo::ROWB + lane * 4) = lo | hi << 16;
         }
     }
 }
@@ -227,12 +226,18 @@ KDA_DEV int warp_lower_bound(const int32_t* __restrict__ cu, int lo, int hi, int
     return lo;
 }
 
-// The part of the packed tokens that split `s` of `S` walks: whole sequences n0 .. n1 - 1,
-// tokens [t0, t1).  (Tokens are counted in 32 bits; offsets of elements in 64.)
+// The part of the tokens that a CTA walks: whole sequences n0 .. n1 - 1, tokens [t0, t1).  (Tokens
+// are counted in 32 bits; offsets of elements in 64.)
 struct ScanSpan {
     int n0, n1, t0, t1;
 };
-KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int lane) {
+// That of split s of S.  Packed sequences go to the splits by their first token.  There the CTAs of a cluster
+// take a part each, on their own, where their sequences can be shared out about evenly: *cluster
+// and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
+// and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
+// tile: 40 sequences of 512 tokens x 4096 take 161 us with CTAs on their own, 204 us in clusters; but
+// 16,384 tokens in one of 41 sequences 292 us on its own, and 174 us in clusters of 2.)
+KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int tile, int* cluster, int* rank, int lane) {
     ScanSpan r;
     if (!a.cu) {
         r.n0 = S == 1 ? 0 : (int)((int64_t)a.B * s / S);
@@ -243,18 +248,42 @@ KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int lane) {
     }
     int end = a.cu[a.n_seqs];
     end = end < 0 ? 0 : (end > (int)a.T ? (int)a.T : end);
-    r.n0 = 0, r.n1 = a.n_seqs, r.t0 = 0, r.t1 = end;
-    if (s > 0) {
-        r.n0 = warp_lower_bound(a.cu, 0, a.n_seqs, (int)((int64_t)end * s / S), lane);
-        r.t0 = r.n0 < a.n_seqs ? a.cu[r.n0] : end;
+    // lane k: the first sequence of part k and its first token
+    const int C = *cluster, part = s * C + (lane < C ? lane : C), parts = S * C;
+    int n = 0, t = 0;
+    if (part == parts) {
+        n = a.n_seqs;
+        t = end;
+    } else if (part > 0) {
+        const int v = (int)((int64_t)end * part / parts);
+        for (int hi = a.n_seqs; n < hi;) {
+            const int mid = n + (hi - n) / 2;
+            if (a.cu[mid] < v) n = mid + 1;
+            else hi = mid;
+        }
+        t = n < a.n_seqs ? a.cu[n] : end;
+        t = t < 0 ? 0 : (t > end ? end : t);
     }
-    if (s + 1 < S) {
-        r.n1 = warp_lower_bound(a.cu, 0, a.n_seqs, (int)((int64_t)end * (s + 1) / S), lane);
-        r.t1 = r.n1 < a.n_seqs ? a.cu[r.n1] : end;
+    auto part_of = [&](int from, int to) {
+        ScanSpan v;
+        v.n0 = __shfl_sync(0xffffffffu, n, from);
+        v.n1 = __shfl_sync(0xffffffffu, n, to);
+        v.t0 = __shfl_sync(0xffffffffu, t, from);
+        v.t1 = __shfl_sync(0xffffffffu, t, to);
+        if (v.t1 < v.t0) v.t1 = v.t0;
+        return v;
+    };
+    r = part_of(0, C);
+    if (C > 1) {
+        const int next = __shfl_down_sync(0xffffffffu, t, 1);
+        const int most = __reduce_max_sync(0xffffffffu, lane < C ? next - t : 0);
+        // on its own, the busiest has at most a quarter more than an equal part, and a few tiles
+        if ((int64_t)most * C <= (int64_t)(r.t1 - r.t0) / 4 * 5 + 4 * C * tile) {
+            r = part_of(*rank, *rank + 1);
+            *cluster = 1;
+            *rank = 0;
+        }
     }
-    if (r.t0 < 0) r.t0 = 0;
-    if (r.t1 > end) r.t1 = end;
-    if (r.t1 < r.t0) r.t1 = r.t0;
     return r;
 }
 
@@ -383,6 +412,11 @@ template <bool PEERS>
 KDA_DEV bool scan_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
     const uint32_t b = smem_u32(bar);
     return scan_try<PEERS>(b, parity) || scan_wait_long<PEERS>(b, parity, status);
+}
+// After a wait has given up: a warp's loads that may still be on their way into its two stages.  How far the
+// barriers had come is not known, so both parities are waited for, each with the limit.
+static __device__ __noinline__ void scan_drain(uint64_t* full) {
+    for (int i = 0; i < 4; ++i) scan_wait<false>(full + (i & 1), i >> 1, nullptr);
 }
 // 16 bytes into a CTA's shared memory, counted on its barrier
 KDA_DEV void st_async16(uint32_t addr, float4 v, uint32_t bar) {
