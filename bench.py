@@ -773,7 +773,7 @@ KERNEL_SOURCES = {
     "kda_chunk_fwd": ("kda_chunk.cu", "kda_sm100.cuh", "kda_slots.h", "kda_tri.cuh"),
     "intra_kernel": ("kda_chunk.cu", "kda_sm100.cuh", "kda_slots.h", "kda_tri.cuh"),
     "chain_kernel": ("kda_chunk.cu", "kda_sm100.cuh", "kda_slots.h"),
-    "decode_multi_kernel": ("kda_decode.cu", "kda_sm100.cuh"),
+    "decode_multi_kernel": ("kda_decode.cu", "kda_row_slot.cuh", "kda_sm100.cuh"),
     "bwd_tc_kernel": ("kda_bwd.cu", "kda_sm100.cuh", "kda_slots.h", "kda_tri.cuh"),
     "chain_bwd_tc_kernel": ("kda_bwd.cu", "kda_sm100.cuh", "kda_slots.h"),
 }

@@ -7,8 +7,8 @@
 // room for (those come from shared memory).  d_norm_weight is summed in a fixed order: each lane over
 // the rows of its half warp, a CTA's half warps through shared memory, the CTAs by a second
 // kernel, whose launch overlaps the first's end.
-// 262,144 rows in bf16: 58.5 us, 5.7 TB/s of the 6.5 that a copy reaches (65.3 us without the loads ahead);
-// fp32 128 us, 5.2 TB/s; 602 rows: 6.2 us, most of it the two launches.
+// 262,144 rows in bf16: 57.4 us, 5.8 TB/s of the 6.5 that a copy reaches (65.3 us without the loads
+// ahead), 2.2 us of it the second kernel; fp32 125 us, 5.4 TB/s; 602 rows: 6.2 us, most of it the two launches.
 #include "kda_launch.h"
 #include "kda_sm100.cuh"
 
@@ -137,9 +137,11 @@ __global__ void __launch_bounds__(256) gate_norm_dw_kernel(const float* __restri
     __shared__ float sh[32][8];
     const int c = threadIdx.x & 7, k = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
     pdl_wait();
-    float t = 0.f;
-#pragma unroll 4
-    for (int i = k; i < n; i += 32) t += partial[(size_t)i * D + col];
+    float v[GNB_MAX_BLOCKS / 32 + 1], t = 0.f;  // all on their way at once
+#pragma unroll
+    for (int i = 0; i <= GNB_MAX_BLOCKS / 32; ++i) v[i] = k + 32 * i < n ? partial[(size_t)(k + 32 * i) * D + col] : 0.f;
+#pragma unroll
+    for (int i = 0; i <= GNB_MAX_BLOCKS / 32; ++i) t += v[i];
     sh[k][c] = t;
     __syncthreads();
     if (threadIdx.x < 8) {
