@@ -374,6 +374,7 @@ KDA_API kda_status kda_gate_norm(const void* o, const void* gate, const float* n
  * slots need 4-byte alignment, all other pointers 16-byte alignment.  D is any
  * size from 1 to 2^28; B * T is at most 2^31 - 65536 tokens.  What is not finite
  * stays in its channel and sequence, where an infinite state may turn to NaN.
+ * A gate below -44 may count as -44 or as -infinity (s is below 1e-19 there).
  *
  *   cu_seqlens   device int32 [n_seqs + 1], cu[0] = 0, non-decreasing,
  *                cu[n_seqs] <= T, or NULL for B sequences of T tokens.  Rows of
@@ -426,8 +427,8 @@ KDA_API kda_status kda_scan_fwd(const void* x, const void* log_alpha, const void
  *   dx, dlog_alpha, dgate  [B, T, D] grad_dtype, contiguous (dgate NULL without
  *                  a gate); d_init_state [N, D] fp32 or NULL (for a sequence
  *                  without tokens d_final_state)
- *   workspace      kda_scan_bwd_workspace_size bytes when chunk_states is NULL;
- *                  otherwise as for kda_scan_fwd
+ *   workspace      kda_scan_bwd_workspace_size bytes when chunk_states is NULL and
+ *                  T > 0; otherwise as for kda_scan_fwd
  */
 KDA_API kda_status kda_scan_bwd(const void* x, const void* log_alpha, const void* gate, const float* init_state,
                                 const void* d_h, const float* d_final_state, const float* chunk_states, void* dx,

@@ -566,6 +566,8 @@ def _check_like(x, dtype, shape, name, t):
 def _check_slots(x, slots, name, n=None):
     torch = _torch()
     if slots is None:
+        if n is None:
+            raise TypeError(f"{name} must be an int32 vector on the device")
         return
     if not slots.is_cuda or slots.device != x.device:
         raise ValueError(f"{name} must be a CUDA tensor on {x.device}")
@@ -573,6 +575,14 @@ def _check_slots(x, slots, name, n=None):
         raise TypeError(f"{name} must be int32")
     if slots.dim() != 1 or (n is not None and slots.numel() != n) or not slots.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector" + (f" of {n}" if n is not None else ""))
+
+
+def _workspace_bytes(x, workspace):
+    if workspace is None:
+        return 0
+    if not workspace.is_cuda or workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {x.device}")
+    return workspace.numel() * workspace.element_size()
 
 
 def _token_rows(x, t, name):
@@ -651,10 +661,10 @@ def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = F
         if chunk_states is True:
             chunk_states = _empty(x, shape, torch.float32)
         _check_like(x, torch.float32, shape, "chunk_states", chunk_states)
-    _check_cuda(workspace)
+    ws_bytes = _workspace_bytes(x, workspace)
     st = load_library().kda_scan_fwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(h), _at(fs),
                                      _at(chunk_states), B, T, D, ldx, ldl, ldg, _at(cu_seqlens), N, _dt(x), _dt(h),
-                                     int(normalize), _at(workspace), 0 if workspace is None else workspace.numel(),
+                                     int(normalize), _at(workspace), ws_bytes,
                                      _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_fwd")
@@ -697,12 +707,12 @@ def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=
     g["d_initial_state"] = _empty(x, (N,) + ch, torch.float32) if want_d_initial_state else None
     if workspace is None and chunk_states is None:
         workspace = _empty(x, (scan_bwd_workspace_size(B, T, D),), torch.uint8)
-    _check_cuda(workspace)
+    ws_bytes = _workspace_bytes(x, workspace)
     st = load_library().kda_scan_bwd(_at(x), _at(log_alpha), _at(gate), _at(initial_state), _at(d_h),
                                      _at(d_final_state), _at(chunk_states), _at(g["dx"]), _at(g["dlog_alpha"]),
                                      _at(g["dgate"]), _at(g["d_initial_state"]), B, T, D, *ld, _at(cu_seqlens), N,
                                      _dt(x), _dt(g["dx"]), int(normalize), _at(workspace),
-                                     0 if workspace is None else workspace.numel(), _here(x.get_device()))
+                                     ws_bytes, _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_bwd")
     return g
@@ -774,7 +784,7 @@ def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=N
     d_o, d_gate (o's shape, fp32 or out_dtype) and d_norm_weight fp32 [128] (None when not
     wanted; without a norm_weight the gradient at a weight of ones)."""
     torch = _torch()
-    _check_cuda(o, workspace)
+    _check_cuda(o)
     if o.shape[-1] != HEAD_DIM:
         raise KdaError(-2, "kda_gate_norm_bwd")
     there = _elsewhere(o, stream)
@@ -794,7 +804,7 @@ def gate_norm_bwd(o, g, d_y, norm_weight=None, *, eps: float = 1e-6, out_dtype=N
     st = load_library().kda_gate_norm_bwd(_at(o), _at(g), _at(d_y), _at(norm_weight), eps, _at(r["d_o"]),
                                           _at(r["d_gate"]), _at(r["d_norm_weight"]), rows, HEAD_DIM, _dt(o),
                                           _dt(r["d_o"]), _at(workspace),
-                                          0 if workspace is None else workspace.numel(), _here(o.get_device()))
+                                          _workspace_bytes(o, workspace), _here(o.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_gate_norm_bwd")
     return r

@@ -346,7 +346,9 @@ kda_status kda_decode_steps_paged(float* state, const int32_t* slots, int n_slot
                                   int H, int dk, int dv, kda_dtype in_dtype, kda_dtype out_dtype, float scale,
                                   const void* gate, const float* norm_weight, float eps, float* step_states,
                                   void* stream) {
-    if (!slots || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    if (n_slots < 0) return KDA_ERR_INVALID_ARG;
+    if ((Bd == 0 && n_steps >= 0) || (n_steps == 0 && Bd >= 0)) return KDA_OK;  // empty tensors may have no address
+    if (!slots) return KDA_ERR_INVALID_ARG;
     return decode_steps_impl(state, slots, n_slots, q, k, v, log_alpha, beta, o, n_steps, Bd, H, dk, dv, in_dtype,
                              out_dtype, scale, gate, norm_weight, eps, step_states, stream);
 }
@@ -472,7 +474,8 @@ kda_status kda_scan_bwd(const void* x, const void* log_alpha, const void* gate, 
     a.chunk_states = const_cast<float*>(chunk_states);
     a.d_final = d_final_state, a.dx = dx, a.dl = dlog_alpha, a.dg = dgate, a.d_init = d_init_state;
     size_t need = 0;
-    if (B > 0 && T >= 0 && D > 0 && !chunk_states) {
+    const bool own_states = !chunk_states && T > 0;  // (no tokens: no states)
+    if (B > 0 && D > 0 && own_states) {
         const kda_status st = kda_scan_bwd_workspace_size(B, T, D, &need);
         if (st != KDA_OK) return st;
     }
@@ -481,7 +484,6 @@ kda_status kda_scan_bwd(const void* x, const void* log_alpha, const void* gate, 
     if (T > 0 && (!d_h || !dx || !dlog_alpha || (gate != nullptr) != (dgate != nullptr))) return KDA_ERR_INVALID_ARG;
     a.n_seqs = n_seqs;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool own_states = !chunk_states;
     if (own_states)
         a.chunk_states = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
     kda::prof_begin(kda::PROF_SCAN_BWD, s);

@@ -114,6 +114,47 @@ def test_longer_batch():
     check(inputs(23, 6, 700, 24, BF))
 
 
+def from_lengths(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [[211, 190, 0, 205, 201, 187, 1, 210, 199], [1500, 3, 40, 1, 77, 129], [5, 0, 31, 1301]],
+                         ids=["even", "long first", "long last"])
+def test_packed_over_clusters(dtype, lens):
+    """CTAs of a cluster with sequences of their own, and with a long one together."""
+    cu = from_lengths(lens)
+    check(inputs(31, 1, cu[-1] + 9, 1020, dtype, N=len(lens)), cu=cu)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [[1024] * 16, [8192] + [128] * 20, [128, 0, 6016, 256, 2048, 1920], [2048] * 6],
+                         ids=["even", "one long", "mixed", "batch"])
+def test_a_sequence_alone_gives_the_same_bits(dtype, lens):
+    """However sequences are shared out: pieces are joined from left to right, tile by tile, and
+    these begin where tiles do."""
+    cu, D = from_lengths(lens), 4096
+    i = inputs(32, 1, cu[-1], D, dtype, N=len(lens))
+    together = run_both(i, cu=cu)
+    if len(set(lens)) == 1:  # the same as a batch of equal lengths
+        b = {k: v.view(len(lens), lens[0], D) if v.dim() == 3 else v for k, v in i.items()}
+        h, fin, gr = run_both(b)
+        assert torch.equal(h.view_as(together[0]), together[0]) and torch.equal(fin, together[1])
+        for k, v in gr.items():
+            assert torch.equal(v.view_as(together[2][k]), together[2][k]), k
+    for n in range(len(lens)):
+        s = slice(cu[n], cu[n + 1])
+        one = {k: v[:, s].contiguous() if v.dim() == 3 else v[n:n + 1].contiguous() for k, v in i.items()}
+        h, fin, gr = run_both(one)
+        assert torch.equal(h, together[0][:, s]) and torch.equal(fin, together[1][n:n + 1]), n
+        for k, v in gr.items():
+            w = together[2][k]
+            assert torch.equal(v, w[n:n + 1] if k == "d_initial_state" else w[:, s]), (n, k)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_behind_the_last_sequence_stay(dtype):
     cu, T, D = [0, 70, 150], 333, 72
@@ -175,6 +216,22 @@ def test_border_decays(norm):
     _, _, gr = run_both(i, norm=norm)
     assert (gr["dlog_alpha"][0, 60:70, 10:20] == 0).all()
     assert (gr["dlog_alpha"][0, 50:52, :10] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm", [False, True])
+def test_open_and_shut_gates(dtype, norm):
+    """sigmoid below 1e-19 (a gate below -44) may count as 0: what that can change is |x| <= 8 summed over 50 tokens."""
+    i = inputs(27, 2, 50, 36, dtype)
+    ends = torch.tensor([-float("inf"), -200.0, -88.0, -60.0, -44.0, -30.0, 30.0, 60.0, 200.0, float("inf")], device="cuda")
+    i["gate"] = ends[torch.arange(i["gate"].numel(), device="cuda") * 7 % 10].view_as(i["gate"]).to(dtype)
+    h, fin, gr = run_both(i, True, norm)
+    r = ref_of(i, True, norm, True, None, True)
+    tiny = 50 * 8 * 1e-19
+    scan_ref.assert_within(h, r["h"], r["h_e"] + tiny, "h")
+    scan_ref.assert_within(fin, r["final"], r["final_e"] + tiny, "final state")
+    for key, ref in (("dx", "dx"), ("dlog_alpha", "dl"), ("dgate", "dgate")):
+        scan_ref.assert_within(gr[key], r[ref], r[ref + "_e"] + 100 * tiny, key)
 
 
 def test_what_a_restart_forgets():
@@ -261,8 +318,10 @@ def test_no_tokens():
     h, fin = kda.scan_fwd(i["x"], i["la"], i["init"])
     assert h.shape == (2, 0, 40) and torch.equal(fin, i["init"])
     assert (kda.scan_fwd(i["x"], i["la"])[1] == 0).all()
-    gr = kda.scan_bwd(i["x"], i["la"], i["dh"], i["init"], i["dfin"])
-    assert torch.equal(gr["d_initial_state"], i["dfin"])
+    cs = kda.scan_fwd(i["x"], i["la"], chunk_states=True)[2]
+    for states in (None, cs):
+        gr = kda.scan_bwd(i["x"], i["la"], i["dh"], i["init"], i["dfin"], chunk_states=states)
+        assert torch.equal(gr["d_initial_state"], i["dfin"])
 
 
 def test_same_bits_every_time():
@@ -298,6 +357,27 @@ def test_side_stream():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(a[0], h) and torch.equal(a[1], fin)
     assert all(torch.equal(a[2][k], gr[k]) for k in gr)
+
+
+def test_two_streams_at_once():
+    a, b = inputs(41, 2, 1000, 520, BF), inputs(42, 1, 1500, 1024, F32)
+    cu = [0, 300, 300, 700, 1500]
+    b["init"], b["dfin"] = b["init"].expand(4, -1).contiguous(), b["dfin"].expand(4, -1).contiguous()
+    calls = [lambda: run_both(a), lambda: run_both(b, cu=cu, given_states=False)]
+    alone = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(6):
+        for f, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(f())
+    torch.cuda.synchronize()
+    for n, (h, fin, gr) in enumerate(got):
+        h0, fin0, gr0 = alone[n % 2]
+        assert torch.equal(h, h0) and torch.equal(fin, fin0)
+        for k in gr:
+            assert torch.equal(gr[k], gr0[k]), k
 
 
 def test_captured_and_replayed():
@@ -342,6 +422,10 @@ def test_binding_refusals():
         kda.scan_bwd(x, la, i["dh"], chunk_states=torch.zeros((2, 40), device="cuda")[:, :40].t())
     with pytest.raises(kda.KdaError):
         kda.scan_bwd(x, la, i["dh"], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.scan_fwd(x, la, workspace=torch.empty(256, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        kda.scan_fwd(x, la, workspace=torch.empty((256, 2), dtype=torch.uint8, device="cuda")[:, 0])
 
 
 # ------------------------------------------------------------------------------------------- single tokens

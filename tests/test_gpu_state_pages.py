@@ -219,6 +219,39 @@ def test_paged_decode_step_is_decode_step():
         kda.decode_step(pool, **one, slots=i32(slots).long())
 
 
+def test_nothing_to_decode():
+    pool = torch.ones((4, 2, 128, 128), device="cuda")
+    tok, gate = kda_tokens(5, 3, 2, 2, BF)
+    for cut in (lambda t: t[:, :0].contiguous(), lambda t: t[:0].contiguous()):
+        none = {k: cut(t) for k, t in tok.items()}
+        n, Bd = none["q"].shape[:2]
+        o, steps = kda.decode_steps(pool, **none, gate=cut(gate), slots=i32([0, 1][:Bd]), step_states=True)
+        assert o.shape == (n, Bd, 2, 128) and steps.shape == (n, Bd, 2, 128, 128)
+        x = torch.zeros((n, Bd, 40), device="cuda")
+        assert kda.scan_decode_steps(torch.zeros((4, 40), device="cuda"), x, x, slots=i32([0, 1][:Bd])).shape == x.shape
+    assert (pool == 1).all()
+
+
+def test_two_streams_at_once():
+    """Two batches of one pool, pages of their own, and page moves of another pool, side by side."""
+    pool = 0.1 * torch.randn((40, 4, 128, 128), device="cuda")
+    want, other = pool.clone(), torch.randn((20, 1000), device="cuda")
+    tok, gate = kda_tokens(6, 2, 16, 4, BF)
+    slots = [i32(range(0, 32, 2)), i32(range(1, 33, 2))]
+    moves = i32(range(10, 20)), i32(range(10))
+    serial = [kda.decode_steps(want, **tok, gate=gate, slots=s) for s in slots for _ in range(3)]
+    kda.state_copy(want_other := other.clone(), moves[0], other, moves[1])
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(3):
+        for n, s in enumerate(streams):
+            got[n].append(kda.decode_steps(pool, **tok, gate=gate, slots=slots[n], stream=s))
+            kda.state_copy(other, moves[0], other, moves[1], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, want) and torch.equal(other, want_other)
+    assert all(torch.equal(a, b) for a, b in zip(got[0] + got[1], serial))
+
+
 def test_pool_larger_than_32_bits():
     """Pages behind 2^32 bytes of the pool."""
     if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
