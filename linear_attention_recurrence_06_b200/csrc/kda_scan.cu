@@ -38,9 +38,9 @@ namespace {
 // inside a token's output; what is carried on goes by the sum of the log-decays.)
 // 16 tokens per warp in bf16: two stages of two CTAs still fit an SM's shared memory, and the hand-overs, which
 // cost as much for 8 tokens, are half as many; the 64 registers of a warp's states and decays are what
-// limits it.  Gated bf16, 4 x 2048 x 4096: 60 us, 4.5 TB/s (without a gate 44 us, 4.5 TB/s); one sequence of
-// 8192: 76 us, 3.5 TB/s, of 32,768: 261 us, 4.1 TB/s (clusters of 4); 125,841 tokens in 16 packed sequences: 803 us,
-// 5.1 TB/s.  What bounds it: schedulers that share two CTAs issue in two of three cycles, and 256 such CTAs
+// limits it.  Gated bf16, 4 x 2048 x 4096: 58 us, 4.6 TB/s (without a gate 41 us, 4.9 TB/s; fp32 92 us, 5.8 TB/s; rows
+// of 4094, without TMA, 123 us); one sequence of 8192: 74 us, 3.6 TB/s, of 32,768: 257 us, 4.2 TB/s (clusters of 4);
+// 125,841 tokens in 16 packed sequences: 765 us, 5.4 TB/s.  What bounds it: schedulers that share two CTAs issue in two of three cycles, and 256 such CTAs
 // leave 40 of 148 SMs with one.
 template <bool BF16, bool GATE>
 struct ScanFwd {
@@ -56,7 +56,8 @@ struct ScanFwd {
     static_assert(2 * (OFF_EX + 4 * 4 * 520 + 1024) <= 228 * 1024, "two CTAs per SM with clusters up to 4");
 };
 
-template <bool BF16, bool GATE, bool NORM>
+// TMA: rows that it can load, of even D.
+template <bool BF16, bool GATE, bool NORM, bool TMA>
 __global__ void __launch_bounds__(SC_THREADS, 2)
 scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
     using K = ScanFwd<BF16, GATE>;
@@ -76,10 +77,10 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);  // the cluster's pieces, [4][cluster][32]
     uint64_t* const sent = reinterpret_cast<uint64_t*>(smem + K::OFF_EX + 4 * cluster * 512);
     uint8_t* const stages = smem + warp * 2 * K::STAGE;
-    const bool even = (D & 1) == 0, tma = width == 16;
+    const bool even = TMA || (D & 1) == 0;
     bool failed = false;
 
-    if (tma && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
+    if (TMA && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x < 32 + K::N_IN) prefetch_tmap(&maps.m[threadIdx.x - 32]);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4 * SC_WARPS + 2; ++i) mbar_init(&bars[i], 1);
         for (int i = 0; i < 4 * cluster; ++i) mbar_init(&sent[i], 1);
@@ -92,7 +93,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     const int by = cluster * TILE;
     auto load = [&](int s, int t) {  // step s, whose tokens begin at t
         uint8_t* const st = stages + (s & 1) * K::STAGE;
-        if (tma) {
+        if constexpr (TMA) {
             if (lane == 0 && s < n_steps) {
                 uint64_t* const b = full + (s & 1);
                 mbar_arrive_expect_tx(b, K::STAGE);
@@ -123,14 +124,14 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         if (s >= at.calm) {
             at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
             // whole rows, and sequences meet at most before the first token and behind the last
-            plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
+            plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1)));
             if (at.starts & 1) {
                 const int n = at.seq_start(0);
                 h0 = a.init ? load2(a.init, n, D, ch) : f2(0.f);
             }
         }
         const uint32_t phase = (s >> 1) & 1;
-        if (tma) {
+        if constexpr (TMA) {
             failed = failed || !scan_wait<false>(full + (s & 1), phase, a.status);
         } else {
             cp_wait<1>();
@@ -245,7 +246,11 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         }
         // the same tokens from that state
         if (plain) {
-            if (a.h && ch < D) {
+            if (a.h && !even) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    store2_odd(a.h, a.out_bf16, (size_t)(tw + i), D, ch, __ffma2_rn(as[i], mine, hs[i]));
+            } else if (a.h && ch < D) {
                 const uint32_t row = (uint32_t)D * (a.out_bf16 ? 2 : 4);
                 uint8_t* const to = static_cast<uint8_t*>(a.h) + (size_t)tw * row + (size_t)ch * (a.out_bf16 ? 2 : 4);
                 if (a.out_bf16) {
@@ -269,7 +274,10 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             for (int i = 0; i < NT; ++i) {
                 const bool from_start = at.starts & ((2u << i) - 2u);
                 const float2 h = from_start ? hs[i] : __ffma2_rn(as[i], mine, hs[i]);
-                if (a.h && at.own >> i & 1) store2(a.h, a.out_bf16, (size_t)(tw + i), D, ch, h);
+                if (a.h && at.own >> i & 1) {
+                    if (TMA) store2_even(a.h, a.out_bf16, (size_t)(tw + i), D, ch, h);
+                    else store2(a.h, a.out_bf16, (size_t)(tw + i), D, ch, h);
+                }
                 if (a.final_state && at.ends >> i & 1) {
                     const int n = at.seq_end(i);
                     if (n >= 0) store2(a.final_state, false, n, D, ch, h);
@@ -278,7 +286,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         }
     }
     cp_wait<0>();
-    if (failed && tma && lane == 0) scan_drain(full);
+    if (failed && TMA && lane == 0) scan_drain(full);
     if (cluster > 1) {
         // The last step's pieces of this and the later CTAs have not been looked at: they have to
         // arrive before this CTA's memory goes, and no CTA leaves while another may write to it.
@@ -408,14 +416,14 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream) {
     int width = 0;
     cudaError_t e = scan_maps(a, in, ld, a.gate ? 3 : 2, a.in_bf16 ? ScanFwd<true, true>::NT : ScanFwd<false, true>::NT, &maps, &width);
     if (e != cudaSuccess) return e;
+#define KDA_SCAN_FWD(BF, TMA)                                                                                      \
+    e = scan_launch<scan_fwd_kernel<BF, G, W, TMA>>(ScanFwd<BF, G>::smem, SC_WARPS * ScanFwd<BF, G>::NT, a, maps, width, \
+                                                    stream)
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
-        if (a.in_bf16)
-            e = scan_launch<scan_fwd_kernel<true, G, W>>(ScanFwd<true, G>::smem, SC_WARPS * ScanFwd<true, G>::NT, a, maps,
-                                                         width, stream);
-        else
-            e = scan_launch<scan_fwd_kernel<false, G, W>>(ScanFwd<false, G>::smem, SC_WARPS * ScanFwd<false, G>::NT, a,
-                                                          maps, width, stream);
+        if (a.in_bf16) { if (width == 16) KDA_SCAN_FWD(true, true); else KDA_SCAN_FWD(true, false); }
+        else           { if (width == 16) KDA_SCAN_FWD(false, true); else KDA_SCAN_FWD(false, false); }
     });
+#undef KDA_SCAN_FWD
     return e;
 }
 

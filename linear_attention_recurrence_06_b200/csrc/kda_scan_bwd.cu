@@ -8,8 +8,9 @@
 // without it the warps' states would have to be handed on as well, before they could begin to
 // walk back), for the factors; then back from zero.  14.5 bytes per value in bf16.  8 tokens per warp: the three
 // factors, the gradient from zero and the products of the decays of 8 tokens already take the 128 registers.
-// Gated bf16, 4 x 2048 x 4096: 101 us, 4.6 TB/s (114 us with the kept states loaded by plain loads); one sequence of
-// 8192: 135 us, 3.5 TB/s, of 32,768: 499 us, 3.8 TB/s; 125,841 tokens in 16 packed sequences: 1.5 ms, 4.8 TB/s.
+// Gated bf16, 4 x 2048 x 4096: 97 us, 5.0 TB/s (without a gate 68 us; fp32 158 us, 6.1 TB/s); one sequence of 8192: 128 us,
+// 3.8 TB/s, of 32,768: 472 us, 4.1 TB/s; 125,841 tokens in 16 packed sequences: 1.46 ms, 5.1 TB/s.  The kept states came
+// by plain loads at first: 114 us for the first case.
 // Bound by issue slots where two CTAs share an SM, as the forward.
 #include <type_traits>
 
@@ -32,7 +33,8 @@ struct ScanBwd {
     static constexpr int smem(int cluster) { return OFF_EX + 4 * cluster * (512 + 8); }
 };
 
-template <bool BF16, bool GATE, bool NORM>
+// TMA: rows that it can load, of even D.
+template <bool BF16, bool GATE, bool NORM, bool TMA>
 __global__ void __launch_bounds__(SC_THREADS, 2)
 scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
     using K = ScanBwd<BF16, GATE>;
@@ -52,10 +54,10 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     float4* const ex = reinterpret_cast<float4*>(smem + K::OFF_EX);  // the cluster's pieces, [4][cluster][32]
     uint64_t* const sent = reinterpret_cast<uint64_t*>(smem + K::OFF_EX + 4 * cluster * 512);
     uint8_t* const stages = smem + warp * 2 * K::STAGE;
-    const bool even = (D & 1) == 0, tma = width == 16;
+    const bool even = TMA || (D & 1) == 0;
     bool failed = false;
 
-    if (tma && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x <= 32 + K::N_IN)
+    if (TMA && n_steps > 0 && threadIdx.x >= 32 && threadIdx.x <= 32 + K::N_IN)
         prefetch_tmap(threadIdx.x < 32 + K::N_IN ? &maps.m[threadIdx.x - 32] : &maps.states);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4 * SC_WARPS + 2; ++i) mbar_init(&bars[i], 1);
@@ -70,7 +72,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     const int by = -cluster * TILE;
     auto load = [&](int s, int t) {  // step s, whose tokens begin at t
         uint8_t* const st = stages + (s & 1) * K::STAGE;
-        if (tma) {
+        if constexpr (TMA) {
             if (lane == 0 && s < n_steps) {
                 const int y = t < 0 ? 0 : t;  // no tokens: any rows do
                 uint64_t* const b = full + (s & 1);
@@ -103,14 +105,14 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         if (s >= at.calm) at = scan_see<NT>(a, sp, s, tw, by, reinterpret_cast<int*>(ab + warp * 32));
         const uint32_t phase = (s >> 1) & 1;
         // whole rows, and sequences meet at most before the first token and behind the last
-        const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1))) && even;
+        const bool plain = at.own == (1u << NT) - 1u && !(at.starts & ~1u) && !(at.ends & ~(1u << (NT - 1)));
         float2 c_end = f2(0.f);
         const bool ends_here = at.ends >> (NT - 1) & 1;
         if (ends_here) {
             const int n = at.seq_end(NT - 1);
             if (a.d_final && n >= 0) c_end = load2(a.d_final, n, D, ch);
         }
-        if (tma) {
+        if constexpr (TMA) {
             failed = failed || !scan_wait<false>(full + (s & 1), phase, a.status);
         } else {
             cp_wait<1>();
@@ -240,7 +242,15 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
 
         if (plain) {
             const float2 g0 = __ffma2_rn(as[0], mine, gs[0]);
-            if (ch < D) {
+            if (!even) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float2 G = __ffma2_rn(as[i], mine, gs[i]);
+                    store2_odd(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
+                    store2_odd(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
+                    if (GATE) store2_odd(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
+                }
+            } else if (ch < D) {
                 const uint32_t es = a.out_bf16 ? 2 : 4, row = (uint32_t)D * es;
                 const size_t off = (size_t)tw * row + (size_t)ch * es;
                 uint8_t* const px = static_cast<uint8_t*>(a.dx) + off;
@@ -279,7 +289,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const bool from_end = at.ends & (((1u << (NT - 1)) - 1u) & ~((1u << i) - 1u));
                 const float2 G = from_end ? gs[i] : __ffma2_rn(as[i], mine, gs[i]);
                 if (!(at.own >> i & 1)) continue;
-                if (!BF16 && even) {  // in line where the registers allow it
+                if (TMA || (!BF16 && even)) {  // in line where the registers allow it: 101 -> 97 us, 4 x 2048 x 4096
                     store2_even(a.dx, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kx[i]));
                     store2_even(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
                     if (GATE) store2_even(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
@@ -296,7 +306,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         }
     }
     cp_wait<0>();
-    if (failed && tma && lane == 0) scan_drain(full);
+    if (failed && TMA && lane == 0) scan_drain(full);
     if (cluster > 1) {
         // The last step's pieces of this and the later CTAs have not been looked at: they have to
         // arrive before this CTA's memory goes, and no CTA leaves while another may write to it.
@@ -336,14 +346,13 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, bool own_states, cudaStream_t str
     if (width == 16 && a.D % 4 != 0) width = 4;
     if (width == 16 && chunks > 0 && !make_scan_map(&maps.states, a.chunk_states, chunks, a.D, a.D, 1, false))
         return cudaErrorInvalidValue;
+#define KDA_SCAN_BWD(BF, TMA) \
+    e = scan_launch<scan_bwd_kernel<BF, G, W, TMA>>(ScanBwd<BF, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width, stream)
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
-        if (a.in_bf16)
-            e = scan_launch<scan_bwd_kernel<true, G, W>>(ScanBwd<true, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width,
-                                                         stream);
-        else
-            e = scan_launch<scan_bwd_kernel<false, G, W>>(ScanBwd<false, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width,
-                                                          stream);
+        if (a.in_bf16) { if (width == 16) KDA_SCAN_BWD(true, true); else KDA_SCAN_BWD(true, false); }
+        else           { if (width == 16) KDA_SCAN_BWD(false, true); else KDA_SCAN_BWD(false, false); }
     });
+#undef KDA_SCAN_BWD
     return e;
 }
 

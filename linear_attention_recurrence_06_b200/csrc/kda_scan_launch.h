@@ -24,15 +24,15 @@ namespace kda {
 // [rows, cols] tensor, rows `ld` elements apart, box of a warp's tokens, zeros outside
 bool make_scan_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool bf16);
 
-// The widest copy that every input's address and token stride allow (16: TMA), and the tensor
-// maps for it.
+// The widest copy that every input's address and token stride allow (16: TMA, where D is even), and
+// the tensor maps for it.
 inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int64_t* ld, int n, int box_rows,
                              ScanMaps* maps, int* width) {
     memset(maps, 0, sizeof(*maps));
     const int64_t tokens = a.cu ? a.T : (int64_t)a.B * a.T;
     uintptr_t all = 0;
     for (int i = 0; i < n; ++i) all |= reinterpret_cast<uintptr_t>(in[i]) | (uintptr_t)(ld[i] * (a.in_bf16 ? 2 : 4));
-    *width = all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
+    *width = all % 16 == 0 && a.D % 2 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
     if (*width == 16 && tokens > 0)
         for (int i = 0; i < n; ++i)
             if (!make_scan_map(&maps->m[i], in[i], tokens, a.D, ld[i], box_rows, a.in_bf16)) return cudaErrorInvalidValue;
@@ -46,10 +46,10 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
 // once: a second wave doubles the time (16 clusters of 8, of which not all find room,
 // took 67 us for 8192 x 1024 values; as clusters of 7, 42 us).
 // Work that fills the GPU is cut finer, into up to 4 times as many splits, so that SMs which
-// have done their part find more (16 x 8192 x 4096: 813 -> 699 us, 6 x 4096 x 4096: 212 -> 167 us;
-// 125,841 tokens in 16 packed sequences x 4096, in 8 splits of 2 instead of 1 of 4: 1,042 -> 803 us),
-// as long as a CTA has 2,048 tokens, about 20 us: its start costs several (4,620 tokens x 1000 in
-// splits of 144: 38 us, of 288: 31 us).
+// have done their part find more (14 % off 16 x 8192 x 4096, 21 % off 6 x 4096 x 4096, 23 % off 125,841
+// tokens in 16 packed sequences x 4096, in 8 splits of 2 instead of 1 of 4), as long as a CTA
+// has 2,048 tokens, about 20 us: its start costs several (4,620 tokens x 1000 take a fifth longer
+// in splits of 144 than of 288).
 constexpr int64_t SC_PART_TOKENS = 2048;
 template <auto KERNEL>
 cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const ScanMaps& maps, int width,

@@ -18,7 +18,7 @@
 // keep enough loads in flight, time has to be split; a cluster does that in one
 // pass over the data, without flags in global memory and without a second launch.  (A warp's
 // piece handed to all others by itself instead of along the chain took 84 us for the case that
-// takes 60 us in kda_scan.cu.)
+// kda_scan.cu names first, then at 59 us.)
 #pragma once
 #include "kda_scan.cuh"
 #include "kda_scan.h"
@@ -131,7 +131,8 @@ KDA_DEV float4 scan_join2(float4 all, float4 v) {
 // ---- loads
 // A warp's NT rows of one tensor come by TMA where its rows are 16-byte aligned (zeros behind the
 // last row and channel), else by asynchronous copies of 4 bytes, or by plain loads of odd
-// rows of 2-byte values; tokens outside [t0, t1) and channels from D on become zeros.
+// rows of 2-byte values; the kernels are compiled without those, too, which take registers from
+// the TMA path (4 x 2048 x 4096 forward: 60 us with them, 58 us without); tokens outside [t0, t1) and channels from D on become zeros.
 KDA_DEV void cp_async4_zfill(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -145,25 +146,40 @@ __device__ __noinline__ void load_rows(uint8_t* dst, const void* base, int64_t l
     using Geo = ScanGeo<BF16>;
     constexpr int ES = Geo::ES;
     const uint8_t* const src = static_cast<const uint8_t*>(base);
-    for (int i = 0; i < NT; ++i) {
-        const int t = tw + i;
-        const bool row_in = t >= t0 && t < t1;
-        if (!BF16 || width == 4) {
+    const bool whole = tw >= t0 && tw + NT <= t1;
+    if (!BF16 || width == 4) {
 #pragma unroll
-            for (int k = 0; k < Geo::ROWB / 128; ++k) {
-                const int ch = ch0 + (lane + 32 * k) * (4 / ES);
-                const int left = (D - ch) * ES, n = left < 0 ? 0 : (left > 4 ? 4 : left);
-                const bool in = row_in && n > 0;
-                cp_async4_zfill(smem_u32(dst + i * Geo::ROWB + (lane + 32 * k) * 4),
-                                in ? src + ((size_t)t * ld + ch) * ES : src, in ? n : 0);
+        for (int k = 0; k < Geo::ROWB / 128; ++k) {
+            const int ch = ch0 + (lane + 32 * k) * (4 / ES);
+            const int left = (D - ch) * ES, n = left < 0 ? 0 : (left > 4 ? 4 : left);
+            const uint32_t to = smem_u32(dst + (lane + 32 * k) * 4);
+            if (whole) {
+                const uint8_t* p = n > 0 ? src + ((size_t)tw * ld + ch) * ES : src;
+                const int64_t step = n > 0 ? ld * ES : 0;
+#pragma unroll
+                for (int i = 0; i < NT; ++i, p += step) cp_async4_zfill(to + i * Geo::ROWB, p, n);
+            } else {
+                for (int i = 0; i < NT; ++i) {
+                    const int t = tw + i;
+                    const bool in = t >= t0 && t < t1 && n > 0;
+                    cp_async4_zfill(to + i * Geo::ROWB, in ? src + ((size_t)t * ld + ch) * ES : src, in ? n : 0);
+                }
             }
-        } else {
-            const uint16_t* const s = reinterpret_cast<const uint16_t*>(src) + (size_t)(row_in ? t : t0) * ld;
-            const int ch = ch0 + 2 * lane;
-            const uint32_t lo = row_in && ch < D ? s[ch] : 0u;
-            const uint32_t hi = row_in && ch + 1 < D ? s[ch + 1] : 0u;
-            *reinterpret_cast<uint32_t*>(dst + i * Geo::ROWB + lane * 4) = lo | hi << 16;
         }
+    } else {
+        // rows at odd multiples of 2 bytes: no copy fits, but all loads are on their way before the first is needed
+        const int ch = ch0 + 2 * lane;
+        const uint16_t* const s = reinterpret_cast<const uint16_t*>(src) + ch;
+        uint32_t lo[NT], hi[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int t = tw + i;
+            const bool row_in = whole || (t >= t0 && t < t1);
+            lo[i] = row_in && ch < D ? __ldg(s + (size_t)t * ld) : 0u;
+            hi[i] = row_in && ch + 1 < D ? __ldg(s + (size_t)t * ld + 1) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) *reinterpret_cast<uint32_t*>(dst + i * Geo::ROWB + lane * 4) = lo[i] | hi[i] << 16;
     }
 }
 
@@ -201,6 +217,19 @@ KDA_DEV void store2_even(void* base, bool bf16, size_t row, int D, int ch, float
     if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + i) = pack_bf16x2(v.x, v.y);
     else *reinterpret_cast<float2*>(static_cast<float*>(base) + i) = v;
 }
+// The same in line for odd D.
+KDA_DEV void store2_odd(void* base, bool bf16, size_t row, int D, int ch, float2 v) {
+    const size_t i = row * D + ch;
+    if (bf16) {
+        uint16_t* const p = static_cast<uint16_t*>(base) + i;
+        if (ch < D) p[0] = f32_to_bf16(v.x);
+        if (ch + 1 < D) p[1] = f32_to_bf16(v.y);
+    } else {
+        float* const p = static_cast<float*>(base) + i;
+        if (ch < D) p[0] = v.x;
+        if (ch + 1 < D) p[1] = v.y;
+    }
+}
 // The decays of a token's channels ch, ch + 1 from global memory (for the few that begin a sequence).
 template <bool BF16>
 __device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
@@ -237,8 +266,8 @@ struct ScanSpan {
 // take a part each, on their own, where their sequences can be shared out about evenly: *cluster
 // and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
 // and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
-// tile: 40 sequences of 512 tokens x 4096 take 161 us with CTAs on their own, 204 us in clusters; but
-// 16,384 tokens in one of 41 sequences 292 us on its own, and 174 us in clusters of 2.)
+// tile: 40 sequences of 512 tokens x 4096 take 151 us with CTAs on their own, a quarter more in clusters; but
+// 16,384 tokens in one of 41 sequences two thirds more on their own than the 164 us in clusters of 2.)
 KDA_DEV ScanSpan scan_span(const ScanArgs& a, int s, int S, int tile, int* cluster, int* rank, int lane) {
     ScanSpan r;
     if (!a.cu) {
