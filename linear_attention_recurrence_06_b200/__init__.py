@@ -817,8 +817,7 @@ def _pool_dims(t, layered, name):
         raise ValueError(f"{name} must be [{'layers, ' if layered else ''}pages, ...]")
     page = math.prod(t.shape[lead:]) * t.element_size()
     L, P = (t.shape[0], t.shape[1]) if layered else (1, t.shape[0])
-    inner = t[0] if layered and L > 0 else t
-    if not inner.is_contiguous():
+    if not t.is_contiguous() and not (layered and L > 0 and t[0].is_contiguous()):
         raise ValueError(f"the pages of {name} must be contiguous, one behind the other")
     return L, P, page, t.stride(0) * t.element_size() if layered else 0
 
@@ -904,8 +903,8 @@ def state_compact(live, *, stream=None):
         with there:
             return state_compact(live)
     P = live.numel()
-    r = {k: _empty(live, (P,), torch.int32) for k in ("dst_slots", "src_slots", "new_slots")}
-    r["n_live"] = _empty(live, (1,), torch.int32)
+    parts = _empty(live, (3 * P + 1,), torch.int32).split((P, P, P, 1))  # one allocation
+    r = dict(zip(("dst_slots", "src_slots", "new_slots", "n_live"), parts))
     st = load_library().kda_state_compact(_at(live), P, _at(r["dst_slots"]), _at(r["src_slots"]), _at(r["new_slots"]),
                                           _at(r["n_live"]), _here(live.get_device()))
     if st != KDA_OK:

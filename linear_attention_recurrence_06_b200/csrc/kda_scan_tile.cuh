@@ -131,8 +131,9 @@ KDA_DEV float4 scan_join2(float4 all, float4 v) {
 // ---- loads
 // A warp's NT rows of one tensor come by TMA where its rows are 16-byte aligned (zeros behind the
 // last row and channel), else by asynchronous copies of 4 bytes, or by plain loads of odd
-// rows of 2-byte values; the kernels are compiled without those, too, which take registers from
-// the TMA path (4 x 2048 x 4096 forward: 60 us with them, 58 us without); tokens outside [t0, t1) and channels from D on become zeros.
+// rows of 2-byte values; tokens outside [t0, t1) and channels from D on become zeros.  TMA has kernels
+// of its own: the calls of the others take registers from it (4 x 2048 x 4096 forward: 60 us with
+// them, 58 us without).
 KDA_DEV void cp_async4_zfill(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
