@@ -64,6 +64,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     constexpr int NT = K::NT, TILE = SC_WARPS * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
     const int ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
     int rank = blockIdx.x % cluster;
     const ScanSpan sp = scan_span(a, blockIdx.y, gridDim.y, TILE, &cluster, &rank, lane);  // changes cluster and rank, too
@@ -112,6 +113,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
     };
     load(0, tw);
     load(1, tw + by);
+    pdl_wait();  // the status word is written behind it
     if (cluster > 1) cluster_sync_all();  // every CTA's barriers are set up before another writes to them
 
     ScanSeen at;
@@ -307,9 +309,12 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
 }
 
 __global__ void scan_check_cu_kernel(const int32_t* cu, int n_seqs, int64_t T, uint32_t* status) {
-    bool bad = threadIdx.x == 0 && cu[0] != 0;
-    for (int i = threadIdx.x; i < n_seqs; i += blockDim.x) bad |= cu[i + 1] < cu[i] || cu[i + 1] > T;
-    if (__syncthreads_or(bad) && threadIdx.x == 0) *status = 2u;
+    pdl_trigger();
+    bool bad = cu && threadIdx.x == 0 && cu[0] != 0;
+    if (cu)
+        for (int i = threadIdx.x; i < n_seqs; i += blockDim.x) bad |= cu[i + 1] < cu[i] || cu[i + 1] > T;
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *status = bad ? 2u : 0u;
 }
 
 // Single tokens: V channels of one row per thread (4 where D allows 16-byte states), the state read
@@ -399,8 +404,6 @@ scan_decode_kernel(float* state, const void* __restrict__ x, const void* __restr
 }  // namespace
 
 cudaError_t launch_scan_check(const ScanArgs& a, cudaStream_t stream) {
-    cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream);
-    if (e != cudaSuccess || !a.cu) return e;
     scan_check_cu_kernel<<<1, 256, 0, stream>>>(a.cu, a.n_seqs, a.T, a.status);
     return cudaGetLastError();
 }
@@ -418,7 +421,7 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
 #define KDA_SCAN_FWD(BF, TMA)                                                                                      \
     e = scan_launch<scan_fwd_kernel<BF, G, W, TMA>>(ScanFwd<BF, G>::smem, SC_WARPS * ScanFwd<BF, G>::NT, a, maps, width, \
-                                                    stream)
+                                                    a.status != nullptr, stream)
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
         if (a.in_bf16) { if (width == 16) KDA_SCAN_FWD(true, true); else KDA_SCAN_FWD(true, false); }
         else           { if (width == 16) KDA_SCAN_FWD(false, true); else KDA_SCAN_FWD(false, false); }

@@ -38,7 +38,7 @@ struct ScanMaps {
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);
 cudaError_t launch_scan_bwd(const ScanArgs& a, bool own_states, cudaStream_t stream);  // own_states: computes chunk_states first
-// clears the status word and records what contradicts in cu
+// sets the status word: what contradicts in cu
 cudaError_t launch_scan_check(const ScanArgs& a, cudaStream_t stream);
 cudaError_t launch_scan_decode(float* state, const void* x, const void* log_alpha, const void* gate, void* h,
                                const int32_t* slots, int n_slots, int n_steps, int Bd, int D, bool in_bf16,

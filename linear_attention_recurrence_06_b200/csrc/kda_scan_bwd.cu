@@ -79,6 +79,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 mbar_arrive_expect_tx(b, K::STAGE);
 #pragma unroll
                 for (int i = 0; i < K::N_IN; ++i) tma_load_2d(st + i * K::ROWS, &maps.m[i], ch0, y, b);
+                if (s == 0) pdl_wait();  // the kernel that writes the states
                 tma_load_2d(st + K::N_IN * K::ROWS, &maps.states, ch0, y / SCAN_CHUNK, b);
             }
         } else {
@@ -93,8 +94,10 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             cp_commit();
         }
     };
+    if (!TMA) pdl_wait();
     load(0, tw);
     load(1, tw + by);
+    pdl_wait();
     if (cluster > 1) cluster_sync_all();  // every CTA's barriers are set up before another writes to them
 
     ScanSeen at;
@@ -347,7 +350,8 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, bool own_states, cudaStream_t str
     if (width == 16 && chunks > 0 && !make_scan_map(&maps.states, a.chunk_states, chunks, a.D, a.D, 1, false))
         return cudaErrorInvalidValue;
 #define KDA_SCAN_BWD(BF, TMA) \
-    e = scan_launch<scan_bwd_kernel<BF, G, W, TMA>>(ScanBwd<BF, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width, stream)
+    e = scan_launch<scan_bwd_kernel<BF, G, W, TMA>>(ScanBwd<BF, G>::smem, SC_WARPS * SCAN_CHUNK, a, maps, width, \
+                                                    own_states || a.status, stream)
     KDA_SCAN_GN(a.gate != nullptr, a.normalize, {
         if (a.in_bf16) { if (width == 16) KDA_SCAN_BWD(true, true); else KDA_SCAN_BWD(true, false); }
         else           { if (width == 16) KDA_SCAN_BWD(false, true); else KDA_SCAN_BWD(false, false); }

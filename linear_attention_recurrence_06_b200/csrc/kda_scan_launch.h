@@ -39,6 +39,10 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
     return cudaSuccess;
 }
 
+// dependent: the kernel ahead is one of the scan's (the check of cu_seqlens, or the forward that writes
+// the chunk states), which lets this one start beside it: launch, set-up and first loads of the call's
+// inputs, which were complete when that one began, overlap its end.
+//
 // Splits of the batch and cluster.  Splitting the batch costs nothing, splitting time costs an
 // exchange per tile, so time is only split where the batch leaves SMs without work; of packed
 // sequences one may be long, so there time comes first, by up to 4, but not by more than
@@ -53,7 +57,7 @@ inline cudaError_t scan_maps(const ScanArgs& a, const void* const* in, const int
 constexpr int64_t SC_PART_TOKENS = 2048;
 template <auto KERNEL>
 cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const ScanMaps& maps, int width,
-                        cudaStream_t stream) {
+                        bool dependent, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};           // devices on which this kernel may use its shared memory
     static std::atomic<int> active[64][SC_MAX_CLUSTER + 1];  // clusters of a size that run at once, + 1
     int dev = 0, sms = 0;
@@ -85,15 +89,17 @@ cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const Sca
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(SC_THREADS);
     cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
     for (;; --cluster) {
         cfg.gridDim = dim3((unsigned)(groups * cluster), (unsigned)splits);
         cfg.dynamicSmemBytes = smem(cluster);
         cfg.numAttrs = cluster > 1 ? 1 : 0;
-        at.val.clusterDim.x = cluster;
+        at[0].val.clusterDim.x = cluster;
         if (cluster == 1) break;
         int n = active[dev][cluster].load(std::memory_order_relaxed) - 1;
         if (n < 0) {
@@ -102,6 +108,7 @@ cudaError_t scan_launch(int (*smem)(int), int tile, const ScanArgs& a, const Sca
         }
         if ((int64_t)groups * at_once <= n) break;
     }
+    if (dependent) cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, KERNEL, a, maps, cluster, width);
 }
 
