@@ -8,8 +8,8 @@
 // without it the warps' states would have to be handed on as well, before they could begin to
 // walk back), for the factors; then back from zero.  14.5 bytes per value in bf16.  8 tokens per warp: the three
 // factors, the gradient from zero and the products of the decays of 8 tokens already take the 128 registers.
-// Gated bf16, 4 x 2048 x 4096: 97 us, 5.0 TB/s (without a gate 68 us; fp32 158 us, 6.1 TB/s); one sequence of 8192: 128 us,
-// 3.8 TB/s, of 32,768: 472 us, 4.1 TB/s; 125,841 tokens in 16 packed sequences: 1.46 ms, 5.1 TB/s.  The kept states came
+// Gated bf16, 4 x 2048 x 4096: 94 us, 5.2 TB/s (without either factor 61 us; fp32 156 us, 6.1 TB/s); one sequence of 8192:
+// 125 us, 3.9 TB/s, of 32,768: 464 us, 4.2 TB/s; 125,841 tokens in 16 packed sequences: 1.41 ms, 5.3 TB/s.  The kept states came
 // by plain loads at first: 114 us for the first case.
 // Bound by issue slots where two CTAs share an SM, as the forward.
 #include <type_traits>
