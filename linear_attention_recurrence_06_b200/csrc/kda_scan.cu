@@ -40,7 +40,7 @@ namespace {
 // cost as much for 8 tokens, are half as many; the 64 registers of a warp's states and decays are what
 // limits it.  Gated bf16, 4 x 2048 x 4096: 55 us, 4.8 TB/s (without either factor 37 us, 5.5 TB/s; fp32 92 us, 5.8 TB/s; rows
 // of 4094, without TMA, 126 us); one sequence of 8192: 73 us, 3.7 TB/s, of 32,768: 254 us, 4.2 TB/s (clusters of 4);
-// 125,841 tokens in 16 packed sequences: 744 us, 5.5 TB/s.  What bounds it: schedulers that share two CTAs issue in two of three cycles, and 256 such CTAs
+// 125,841 tokens in 16 packed sequences: 744 us, 5.5 TB/s.  What bounds it: schedulers that share two CTAs issue in three of four cycles, and 256 such CTAs
 // leave 40 of 148 SMs with one.
 template <bool BF16, bool GATE>
 struct ScanFwd {
