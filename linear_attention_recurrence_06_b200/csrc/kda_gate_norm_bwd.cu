@@ -99,7 +99,9 @@ gate_norm_bwd_kernel(const void* __restrict__ o, const void* __restrict__ g, con
             ss += ov[c] * ov[c];
             s[c] = __fdividef(1.f, 1.f + __expf(-s[c]));
         }
-        const float r = rsqrtf(half_warp_sum(ss) * (1.f / D) + eps);
+        ss = half_warp_sum(ss);
+        // a row past the end is all zeros and adds nothing to dw, with eps = 0 too
+        const float r = in ? rsqrtf(ss * (1.f / D) + eps) : 0.f;
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
