@@ -17,3 +17,27 @@ def test_eps_of_zero(dtype, rows):
     """Rows that no half warp has beside it: 1 / sqrt(0 + 0) of nothing must not reach the weight's sum."""
     o, ga, dy, w = inputs(rows + 100, rows, dtype)
     check(o, ga, dy, w, kda.gate_norm_bwd(o, ga, dy, w, eps=0.0), eps=0.0)
+
+
+def weight_sum_bound(rows, terms_abs):
+    """e (2^-24) times the roundings on a term's way: 45 of its factors (as scan_ref), one per row that a half warp
+    walks (592 CTAs of 16 half warps at most), 16 half warps of a CTA, at most 19 partial sums per thread of the second
+    kernel, 32 of those."""
+    blocks = min(-(-rows // 16), 592)
+    turns = -(-rows // (16 * blocks))
+    return scan_ref.EPS * (45 + turns + 16 + 19 + 32) * terms_abs
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [5000, 9471, 9472, 9473, 18945, 100_003])
+def test_weight_sums_of_every_turn(dtype, rows):
+    """A half warp's rows of one turn or several, all CTAs' sums: no row is missing and none counted twice."""
+    o, ga, dy, w = inputs(rows, rows, dtype)
+    got = kda.gate_norm_bwd(o, ga, dy, w)["d_norm_weight"]
+    terms = dy.double() * torch.sigmoid(ga.double()) * o.double() / (o.double().square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    bound = weight_sum_bound(rows, terms.abs().sum(0))
+    scan_ref.assert_within(got, terms.sum(0), bound, "d_norm_weight")
+    # a turn, a CTA's or a half warp's rows left out would be seen
+    turn = slice(max(0, rows - 9472), rows)
+    for part in (turn, slice(0, rows, 16)):
+        assert ((terms[part].sum(0)).abs() > 2 * bound).float().mean() > 0.5
