@@ -9,6 +9,8 @@
 // kernel, whose launch overlaps the first's end.
 // 262,144 rows in bf16: 57.4 us, 5.8 TB/s of the 6.5 that a copy reaches (65.3 us without the loads
 // ahead), 2.2 us of it the second kernel; fp32 125 us, 5.4 TB/s; 602 rows: 6.2 us, most of it the two launches.
+#include <float.h>
+
 #include "kda_launch.h"
 #include "kda_sm100.cuh"
 
@@ -97,7 +99,7 @@ gate_norm_bwd_kernel(const void* __restrict__ o, const void* __restrict__ g, con
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             ss += ov[c] * ov[c];
-            s[c] = __fdividef(1.f, 1.f + __expf(-s[c]));
+            s[c] = __expf(-s[c]);
         }
         ss = half_warp_sum(ss);
         // a row past the end is all zeros and adds nothing to dw, with eps = 0 too
@@ -105,8 +107,10 @@ gate_norm_bwd_kernel(const void* __restrict__ o, const void* __restrict__ g, con
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
+            const float sig = __fdividef(1.f, 1.f + s[c]);
             ov[c] *= r;                // n
-            y[c] *= s[c];              // dy s
+            y[c] *= sig;               // dy s
+            s[c] = fminf(s[c], FLT_MAX) * sig;  // 1 - s = e^-g s keeps its digits where s is next to 1 (s = 0: times 0)
             dw[c] += y[c] * ov[c];
             y[c] *= sw[sub * 8 + c];   // dn
             dot += y[c] * ov[c];
@@ -115,7 +119,7 @@ gate_norm_bwd_kernel(const void* __restrict__ o, const void* __restrict__ g, con
         if (!in) continue;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            s[c] = y[c] * ov[c] * (1.f - s[c]);
+            s[c] = y[c] * ov[c] * s[c];
             y[c] = r * (y[c] - ov[c] * dot);
         }
         store8<OUT_BF16>(d_o, i, y);

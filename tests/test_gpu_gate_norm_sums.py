@@ -41,3 +41,31 @@ def test_weight_sums_of_every_turn(dtype, rows):
     turn = slice(max(0, rows - 9472), rows)
     for part in (turn, slice(0, rows, 16)):
         assert ((terms[part].sum(0)).abs() > 2 * bound).float().mean() > 0.5
+
+
+@pytest.mark.parametrize("gate", [7.0, 9.0, 12.0, 16.0, 30.0, 80.0])
+def test_gradient_of_open_gates(gate):
+    """1 - sigmoid keeps its digits where the sigmoid is next to 1.  e^-g is off by 2 + 1.173 g ulps (2 e each), the
+    sigmoid beside it by 6 e, n by 11 e, products 4 e: relative to the value."""
+    o, ga, dy, w = inputs(int(gate), 50, F32)
+    ga = gate + 0.1 * ga
+    got = kda.gate_norm_bwd(o, ga, dy, w)["d_gate"]
+    o, ga, dy = (t.double() for t in (o, ga, dy))
+    n = o / (o.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    ref = dy * n * w.double() * torch.sigmoid(ga) * torch.sigmoid(-ga)
+    scan_ref.assert_within(got, ref, scan_ref.EPS * (2 * (2 + 1.173 * ga) + 21) * ref.abs(), "d_gate")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gates_at_both_ends(dtype):
+    """Shut gates and open ones, to infinity: zeros or what is left, no NaN; a NaN stays NaN."""
+    o, ga, dy, w = inputs(3, 16, dtype)
+    ends = torch.tensor([-float("inf"), -200.0, -88.5, -88.0, -87.0, 87.0, 200.0, float("inf")], device="cuda").to(dtype)
+    ga = ends[torch.arange(ga.numel(), device="cuda") * 3 % 8].view_as(ga).clone()
+    r = kda.gate_norm_bwd(o, ga, dy, w)
+    assert all(torch.isfinite(r[k]).all() for k in r)
+    assert (r["d_gate"].abs() <= 1e-36).all() and (r["d_gate"][torch.isinf(ga)] == 0).all()
+    ga[2, 5] = float("nan")
+    r = kda.gate_norm_bwd(o, ga, dy, w)
+    assert torch.isnan(r["d_gate"][2, 5]) and torch.isnan(r["d_o"][2]).all()
+    assert all(torch.isfinite(r[k][torch.arange(16, device="cuda") != 2]).all() for k in ("d_o", "d_gate"))
