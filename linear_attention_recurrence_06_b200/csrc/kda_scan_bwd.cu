@@ -12,6 +12,8 @@
 // 125 us, 3.9 TB/s, of 32,768: 464 us, 4.2 TB/s; 125,841 tokens in 16 packed sequences: 1.41 ms, 5.3 TB/s.  The kept states came
 // by plain loads at first: 114 us for the first case.
 // Bound by issue slots where two CTAs share an SM, as the forward.
+#include <float.h>
+
 #include <type_traits>
 
 #include "kda_scan_launch.h"
@@ -141,12 +143,14 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 if (!own) d = x = f2(0.f);
                 const ScanDecay2 a2 = scan_decay2(d);
                 const float2 A = a2.a;
-                float2 sg = f2(1.f), w = f2(1.f), r = f2(0.f);
+                float2 sg = f2(1.f), sn = f2(0.f), w = f2(1.f), r = f2(0.f);  // s, 1 - s
                 if (GATE) {
                     const float2 g = tile_at<BF16>(st + 3 * K::ROWS, i, lane), y = __fmul2_rn(g, f2(-LOG2E));
-                    const float2 q = __fadd2_rn(f2(ex2_ftz(y.x), ex2_ftz(y.y)), f2(1.f));
+                    const float2 e = f2(ex2_ftz(y.x), ex2_ftz(y.y)), q = __fadd2_rn(e, f2(1.f));
                     sg = f2(rcp_ftz(q.x), rcp_ftz(q.y));
                     if (!own) sg = f2(0.f);
+                    // e^-gate s keeps its digits where s is next to 1 (s = 0: times 0)
+                    sn = __fmul2_rn(f2(fminf(e.x, FLT_MAX), fminf(e.y, FLT_MAX)), sg);
                 }
                 if (NORM) {
                     const float2 n = __fmul2_rn(a2.m, __ffma2_rn(a2.m, f2(-1.f), f2(2.f)));
@@ -156,7 +160,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 }
                 kx[i] = GATE && NORM ? __fmul2_rn(sg, w) : (GATE ? sg : w);
                 const float2 u = GATE || NORM ? __fmul2_rn(kx[i], x) : x;
-                if (GATE) kg[i] = __fmul2_rn(u, __ffma2_rn(sg, f2(-1.f), f2(1.f)));
+                if (GATE) kg[i] = __fmul2_rn(u, sn);
                 if (EDGE && i > 0 && (at.starts >> i & 1)) {
                     const int n = at.seq_start(i);
                     h = a.init ? load2(a.init, n, D, ch) : f2(0.f);

@@ -1,0 +1,44 @@
+"""What the element-wise scan keeps of its digits where a rounding would show: gates next to open, states and gradients
+handed from call to call, decays next to 1 (tests/scan_ref.py derives the bounds that are not derived here)."""
+import pytest
+import torch
+
+import linear_attention_recurrence_06_b200 as kda
+import scan_ref
+from test_gpu_scan import as_cu, inputs, ref_of, run_both
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("gate", [7.0, 9.0, 12.0, 16.0, 30.0])
+def test_gate_gradient_of_open_gates(dtype, norm, gate):
+    """dgate = G u (1 - s) = dx x (1 - s), 1 - s = e^-gate s.  dx's own bound holds 40 e of its G beside what G carries:
+    enough for u's 36 as well.  e^-gate is off by 2 ulps (2 e each) of the hardware's 2^y and gate e of y's two
+    roundings, s by 4 e, products 3 e: relative to 1 - s, a (12 + gate) / 40 part of that bound again.  The reference
+    is dx x / (1 + e^gate): its own 1 - s of 64 bits is off by 2^-53 absolute, 1e-3 of the value at a gate of 30."""
+    i = inputs(int(gate), 2, 150, 72, dtype)
+    i["gate"] = (gate + 0.1 * i["gate"].float()).to(dtype)
+    r = ref_of(i, True, norm, True, None, True)
+    _, _, gr = run_both(i, True, norm)
+    ga = i["gate"].double().cpu()
+    rest = i["x"].double().cpu() * torch.sigmoid(-ga)
+    scan_ref.assert_within(gr["dgate"], rest * r["dx"], rest.abs() * r["dx_e"] * (1 + (12 + ga) / 40), "dgate")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gates_of_infinity(dtype):
+    """A shut gate lets exactly nothing through, also of huge values; an open one has no gradient; NaN stays."""
+    i = inputs(5, 1, 60, 40, dtype)
+    ends = torch.tensor([-float("inf"), -200.0, -89.0, 200.0, float("inf")], device="cuda").to(dtype)
+    i["gate"] = ends[torch.arange(i["gate"].numel(), device="cuda") * 3 % 5].view_as(i["gate"]).clone()
+    shut = i["gate"] < 0
+    i["x"][shut] = 1e30
+    _, _, gr = run_both(i, True, False)
+    assert all(torch.isfinite(t).all() for t in gr.values())
+    assert (gr["dx"][shut] == 0).all() and (gr["dgate"][i["gate"] == float("inf")] == 0).all()
+    i["gate"][0, 30, 7] = float("nan")
+    _, _, gr = run_both(i, True, False)
+    assert torch.isnan(gr["dgate"][0, 30, 7]) and torch.isnan(gr["dx"][0, 30, 7])
