@@ -39,11 +39,12 @@ struct ScanGeo {
 KDA_DEV float2 f2(float x, float y) { return make_float2(x, y); }
 KDA_DEV float2 f2(float x) { return make_float2(x, x); }
 
-// Decays of two channels, `d` = -l >= 0:  a = e^-d by the hardware, and m = 1 - a: its Taylor polynomial to
-// d^5 below 1/8 (the next term is below 2^-24 of m there), above it what a leaves of 1.  A warp's tokens
-// are stepped with a as it is: its error, 2^-22 per token, does not add up beyond them, for what is
-// handed on goes by the sum of the d (scan_piece).  (a = 1 - m below 1/8 is four times as near, and took
-// 57.4 us where this takes 55.5, without normalize 41 and 37 us: 4 x 2048 x 4096 forward.)
+// Decays of two channels, `d` = -l >= 0:  a = e^-d and m = 1 - a.  m is its Taylor polynomial to d^5 below
+// 1/8 (the next term is below 2^-24 of m there), where a = 1 - m; above it a is the hardware's e^-d,
+// and m what that leaves of 1.  A warp's tokens are stepped with a as it is: its rounding does
+// not add up beyond them, for what is handed on goes by the sum of the d (scan_piece).  (The hardware's
+// e^-d below 1/8 too would save 2 us of 57, 4 of 41 without either factor; its errors all go one
+// way there: a state's was 1.5e-7 to 1.9e-7 of it, against 1e-8.)
 constexpr float SCAN_NEAR = 0.125f;
 struct ScanDecay2 {
     float2 a, m;
@@ -56,9 +57,10 @@ KDA_DEV ScanDecay2 scan_decay2(float2 d) {
     const float2 near = __ffma2_rn(__fmul2_rn(t, d), d, d);
     const float2 x = __fmul2_rn(d, f2(-LOG2E));
     const float2 e = f2(ex2_ftz(x.x), ex2_ftz(x.y));
-    const float2 m1 = __ffma2_rn(e, f2(-1.f), f2(1.f));
-    r.m = f2(d.x < SCAN_NEAR ? near.x : m1.x, d.y < SCAN_NEAR ? near.y : m1.y);
-    r.a = e;
+    const float2 m1 = __ffma2_rn(e, f2(-1.f), f2(1.f)), a1 = __ffma2_rn(near, f2(-1.f), f2(1.f));
+    const bool nx = d.x < SCAN_NEAR, ny = d.y < SCAN_NEAR;
+    r.m = f2(nx ? near.x : m1.x, ny ? near.y : m1.y);
+    r.a = f2(nx ? a1.x : e.x, ny ? a1.y : e.y);
     return r;
 }
 // -l of two channels: max(-log_alpha, 0), NaN kept
@@ -265,7 +267,6 @@ struct ScanSpan {
 };
 // That of split s of S.  Packed sequences go to the splits by their first token.  There the CTAs of a cluster
 // take a part each, on their own, where their sequences can be shared out about evenly: *cluster
-// and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
 // and *rank then become 1 and 0.  (Sharing the tiles of all sequences instead costs an exchange per
 // tile: 40 sequences of 512 tokens x 4096 take 149 us with CTAs on their own, a quarter more in clusters; but
 // 16,384 tokens in one of 41 sequences two thirds more on their own than the 161 us in clusters of 2.)
