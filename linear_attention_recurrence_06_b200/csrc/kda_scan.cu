@@ -151,7 +151,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const float2 g = GATE ? tile_at<BF16>(st + 2 * K::ROWS, i, lane) : f2(0.f);
                 const bool own = !EDGE || (at.own >> i & 1);
                 if (!own) d = f2(0.f);
-                const ScanDecay2 a2 = scan_decay2(d);
+                const ScanDecay2 a2 = scan_decay2<!BF16>(d);
                 if (GATE || NORM) u = __fmul2_rn(scan_weight2<GATE, NORM>(a2.m, g), u);
                 if (!own) u = f2(0.f);
                 sum = __fadd2_rn(sum, d);

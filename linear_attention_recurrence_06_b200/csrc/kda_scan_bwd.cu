@@ -141,7 +141,7 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const float2 la = tile_at<BF16>(st, i, lane);
                 float2 x = tile_at<BF16>(st + K::ROWS, i, lane), d = scan_depth2(la);
                 if (!own) d = x = f2(0.f);
-                const ScanDecay2 a2 = scan_decay2(d);
+                const ScanDecay2 a2 = scan_decay2<!BF16>(d);
                 const float2 A = a2.a;
                 float2 sg = f2(1.f), sn = f2(0.f), w = f2(1.f), r = f2(0.f);  // s, 1 - s
                 if (GATE) {

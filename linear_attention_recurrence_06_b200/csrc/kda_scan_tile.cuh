@@ -40,15 +40,18 @@ KDA_DEV float2 f2(float x, float y) { return make_float2(x, y); }
 KDA_DEV float2 f2(float x) { return make_float2(x, x); }
 
 // Decays of two channels, `d` = -l >= 0:  a = e^-d and m = 1 - a.  m is its Taylor polynomial to d^5 below
-// 1/8 (the next term is below 2^-24 of m there), where a = 1 - m; above it a is the hardware's e^-d,
-// and m what that leaves of 1.  A warp's tokens are stepped with a as it is: its rounding does
-// not add up beyond them, for what is handed on goes by the sum of the d (scan_piece).  (The hardware's
-// e^-d below 1/8 too would save 2 us of 57, 4 of 41 without either factor; its errors all go one
-// way there: a state's was 1.5e-7 to 1.9e-7 of it, against 1e-8.)
+// 1/8 (the next term is below 2^-24 of m there), above it what a leaves of 1.  FINE (fp32 tokens): a = 1 - m
+// below 1/8, above it the hardware's e^-d; else the latter everywhere.  A warp's tokens are stepped with a
+// as it is: its rounding does not add up beyond them, for what is handed on goes by the sum of the d
+// (scan_piece).  The hardware's errors, below 2 steps, lean one way: h is off by 1.8e-7 of it (root mean square)
+// instead of 1.2e-7, by 0.9e-7 on average instead of 1e-8.  With fp32 tokens that would reach the caller, and 1 - m costs nothing (90 us,
+// 4 x 2048 x 4096 forward: those kernels wait for memory); with bf16 tokens it is a thousandth of what their own
+// rounding leaves open, and 1 - m would take 55 us for 54, without either factor 40 for 35.
 constexpr float SCAN_NEAR = 0.125f;
 struct ScanDecay2 {
     float2 a, m;
 };
+template <bool FINE>
 KDA_DEV ScanDecay2 scan_decay2(float2 d) {
     ScanDecay2 r;
     float2 t = __ffma2_rn(d, f2(1.f / 120.f), f2(-1.f / 24.f));
@@ -60,7 +63,7 @@ KDA_DEV ScanDecay2 scan_decay2(float2 d) {
     const float2 m1 = __ffma2_rn(e, f2(-1.f), f2(1.f)), a1 = __ffma2_rn(near, f2(-1.f), f2(1.f));
     const bool nx = d.x < SCAN_NEAR, ny = d.y < SCAN_NEAR;
     r.m = f2(nx ? near.x : m1.x, ny ? near.y : m1.y);
-    r.a = f2(nx ? a1.x : e.x, ny ? a1.y : e.y);
+    r.a = FINE ? f2(nx ? a1.x : e.x, ny ? a1.y : e.y) : e;
     return r;
 }
 // -l of two channels: max(-log_alpha, 0), NaN kept
@@ -110,7 +113,7 @@ KDA_DEV float2 scan_step2(float2 p, float2 h, float2 u) {
                             __uint_as_float(__float_as_uint(h.y) & (uint32_t)(__float_as_int(p.y) >> 31))));
 }
 KDA_DEV float4 scan_piece(bool cut, float2 depth, float2 b) {
-    const ScanDecay2 d = scan_decay2(depth);
+    const ScanDecay2 d = scan_decay2<true>(depth);
     const float2 p = f2(depth.x < SCAN_NEAR ? -d.m.x : d.a.x, depth.y < SCAN_NEAR ? -d.m.y : d.a.y);
     return make_float4(cut ? SC_CUT : p.x, cut ? SC_CUT : p.y, b.x, b.y);
 }
@@ -238,7 +241,7 @@ template <bool BF16>
 __device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
     const size_t i = (size_t)t * ld + ch;
     const float2 d = scan_depth2(f2(ch < D ? ld_in<BF16>(log_alpha, i) : 0.f, ch + 1 < D ? ld_in<BF16>(log_alpha, i + 1) : 0.f));
-    return scan_decay2(d).a;
+    return scan_decay2<!BF16>(d).a;
 }
 KDA_DEV float2 load2(const float* base, size_t row, int D, int ch) {
     const size_t i = row * D + ch;
