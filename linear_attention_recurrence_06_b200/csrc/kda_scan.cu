@@ -154,17 +154,23 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 const ScanDecay2 a2 = scan_decay2<!BF16>(d);
                 if (GATE || NORM) u = __fmul2_rn(scan_weight2<GATE, NORM>(a2.m, g), u);
                 if (!own) u = f2(0.f);
-                sum = __fadd2_rn(sum, d);
+                // up to a sequence's last token, for its final state
+                if (!EDGE || !(at.ends & ((1u << i) - 1u))) sum = __fadd2_rn(sum, d);
                 if (i == 0) {
                     hs[0] = u;
                     as[0] = a2.a;
                 } else {
-                    hs[i] = __ffma2_rn(a2.a, hs[i - 1], u);
+                    if (!EDGE) {
+                        hs[i] = __ffma2_rn(a2.a, hs[i - 1], u);
+                    } else {  // the whole of a short sequence, perhaps, which the caller may go on with
+                        float2 h = hs[i - 1];
+                        if (at.starts >> i & 1) {
+                            const int n = at.seq_start(i);
+                            h = a.init ? load2(a.init, n, D, ch) : f2(0.f);
+                        }
+                        hs[i] = scan_step2(scan_p2(d, a2), h, u);
+                    }
                     as[i] = __fmul2_rn(a2.a, as[i - 1]);
-                }
-                if (EDGE && i > 0 && (at.starts >> i & 1)) {
-                    const int n = at.seq_start(i);
-                    hs[i] = __ffma2_rn(a2.a, a.init ? load2(a.init, n, D, ch) : f2(0.f), u);
                 }
             }
         };
@@ -269,7 +275,7 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             }
             if (at.ends && a.final_state) {
                 const int n = at.seq_end(NT - 1);
-                if (n >= 0) store2(a.final_state, false, n, D, ch, __ffma2_rn(as[NT - 1], mine, hs[NT - 1]));
+                if (n >= 0) store2(a.final_state, false, n, D, ch, scan_fold2(scan_piece(false, sum, hs[NT - 1]), mine));
             }
         } else {
 #pragma unroll
@@ -282,7 +288,9 @@ scan_fwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 }
                 if (a.final_state && at.ends >> i & 1) {
                     const int n = at.seq_end(i);
-                    if (n >= 0) store2(a.final_state, false, n, D, ch, h);
+                    if (n >= 0)
+                        store2(a.final_state, false, n, D, ch,
+                               from_start ? hs[i] : scan_fold2(scan_piece(false, sum, hs[i]), mine));
                 }
             }
         }

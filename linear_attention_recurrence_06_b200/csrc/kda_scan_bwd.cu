@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(SC_THREADS, 2)
 scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int cluster, int width) {
     using K = ScanBwd<BF16, GATE>;
     constexpr int NT = K::NT, TILE = SC_WARPS * NT;
+    constexpr uint32_t ALL_BUT_LAST = (1u << (NT - 1)) - 1u;  // of a warp's tokens
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ch0 = blockIdx.x / cluster * SC_CH, ch = ch0 + 2 * lane, D = a.D;
@@ -190,8 +191,24 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                 P = __fmul2_rn(P, A);
             }
         };
-        if (plain) runs(std::false_type{});
-        else runs(std::true_type{});
+        if (plain) {
+            runs(std::false_type{});
+        } else {
+            runs(std::true_type{});
+            // What goes beyond this call, or may, is stepped without the roundings of decays, which would add up where the
+            // caller hands d_init on to an earlier call: what the tokens up to the first end hand on to an earlier warp,
+            // and the d_init of sequences that are all here.
+            for (uint32_t m = at.ends & ALL_BUT_LAST; m; m &= m - 1) {
+                const int e = __ffs(m) - 1, n = at.seq_end(e), i0 = 31 - __clz(at.starts & ((2u << e) - 1u));  // or -1
+                if (i0 < 0 ? !a.d_final : !a.d_init) continue;
+                float2 v = a.d_final && n >= 0 ? load2(a.d_final, n, D, ch) : f2(0.f);
+#pragma unroll 1
+                for (int i = e; i >= (i0 < 0 ? 0 : i0); --i)
+                    v = scan_back(scan_depth2(tile_at<BF16>(st, i, lane)), tile_at<BF16>(st + 2 * K::ROWS, i, lane), v);
+                if (i0 < 0) c = v;
+                else if (a.d_init && n >= 0) store2_odd(a.d_init, false, n, D, ch, v);
+            }
+        }
         float4 piece = scan_piece(false, sum, c);
         if (at.ends) {  // nothing of what lies behind gets through
             const float2 b = at.ends == 1u << (NT - 1) ? scan_fold2(piece, c_end) : c;
@@ -207,8 +224,8 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
             before = ab[(warp - 1) * 32 + lane];
             piece = scan_join2(before, piece);
         }
+        ab[warp * 32 + lane] = piece;
         if (warp < SC_WARPS - 1) {
-            ab[warp * 32 + lane] = piece;
             __syncwarp();
             if (lane == 0) mbar_arrive(given + (s & 1));
         } else {
@@ -248,7 +265,6 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
         if (ends_here) mine = c_end;
 
         if (plain) {
-            const float2 g0 = __ffma2_rn(as[0], mine, gs[0]);
             if (!even) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -285,15 +301,10 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                     }
                 }
             }
-            if ((at.starts & 1) && a.d_init) {
-                const int n = at.seq_start(0);
-                const float2 la = tile_decay<BF16>(a.log_alpha, a.ld_l, tw, D, ch);
-                store2(a.d_init, false, n, D, ch, __fmul2_rn(la, g0));
-            }
         } else {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const bool from_end = at.ends & (((1u << (NT - 1)) - 1u) & ~((1u << i) - 1u));
+                const bool from_end = at.ends & ALL_BUT_LAST & ~((1u << i) - 1u);
                 const float2 G = from_end ? gs[i] : __ffma2_rn(as[i], mine, gs[i]);
                 if (!(at.own >> i & 1)) continue;
                 if (TMA || (!BF16 && even)) {  // in line where the registers allow it: 101 -> 97 us, 4 x 2048 x 4096
@@ -305,10 +316,19 @@ scan_bwd_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps, int clu
                     store2(a.dl, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kl[i]));
                     if (GATE) store2(a.dg, a.out_bf16, (size_t)(tw + i), D, ch, __fmul2_rn(G, kg[i]));
                 }
-                if ((at.starts >> i & 1) && a.d_init) {
-                    const int n = at.seq_start(i);
-                    store2(a.d_init, false, n, D, ch, __fmul2_rn(tile_decay<BF16>(a.log_alpha, a.ld_l, tw + i, D, ch), G));
+            }
+        }
+        if (a.d_init && at.starts) {
+            const int i = 31 - __clz(at.starts);  // the start whose sequence goes on behind the warp's tokens
+            if (!(at.ends & ALL_BUT_LAST & ~((1u << i) - 1u))) {
+                float2 v;
+                if (i == 0) {  // all pieces up to the sequence's first token over what lies behind the tile
+                    const float4 all = ab[warp * 32 + lane];
+                    v = scan_fold2(all, base[(s & 1) * 32 + lane], scan_is_cut(all));
+                } else {
+                    v = scan_d_init<BF16>(a.log_alpha, a.ld_l, a.d_h, a.ld_dh, tw + i, __popc(at.own >> i), D, ch, mine);
                 }
+                store2(a.d_init, false, at.seq_start(i), D, ch, v);
             }
         }
     }

@@ -42,8 +42,8 @@ KDA_DEV float2 f2(float x) { return make_float2(x, x); }
 // Decays of two channels, `d` = -l >= 0:  a = e^-d and m = 1 - a.  m is its Taylor polynomial to d^5 below
 // 1/8 (the next term is below 2^-24 of m there), above it what a leaves of 1.  FINE (fp32 tokens): a = 1 - m
 // below 1/8, above it the hardware's e^-d; else the latter everywhere.  A warp's tokens are stepped with a
-// as it is: its rounding does not add up beyond them, for what is handed on goes by the sum of the d
-// (scan_piece).  The hardware's errors, below 2 steps, lean one way: h is off by 1.8e-7 of it (root mean square)
+// as it is: its rounding does not add up beyond them, for what is handed on, to the next warp or to the caller
+// and a next call, goes by the sum of the d (scan_piece) or by steps of scan_p2.  The hardware's errors, below 2 steps, lean one way: h is off by 1.8e-7 of it (root mean square)
 // instead of 1.2e-7, by 0.9e-7 on average instead of 1e-8.  With fp32 tokens that would reach the caller, and 1 - m costs nothing (90 us,
 // 4 x 2048 x 4096 forward: those kernels wait for memory); with bf16 tokens it is a thousandth of what their own
 // rounding leaves open, and 1 - m would take 55 us for 54, without either factor 40 for 35.
@@ -112,9 +112,12 @@ KDA_DEV float2 scan_step2(float2 p, float2 h, float2 u) {
     return __fadd2_rn(t, f2(__uint_as_float(__float_as_uint(h.x) & (uint32_t)(__float_as_int(p.x) >> 31)),
                             __uint_as_float(__float_as_uint(h.y) & (uint32_t)(__float_as_int(p.y) >> 31))));
 }
+// e^-depth of both channels in scan_decay's form
+KDA_DEV float2 scan_p2(float2 depth, const ScanDecay2& d) {
+    return f2(depth.x < SCAN_NEAR ? -d.m.x : d.a.x, depth.y < SCAN_NEAR ? -d.m.y : d.a.y);
+}
 KDA_DEV float4 scan_piece(bool cut, float2 depth, float2 b) {
-    const ScanDecay2 d = scan_decay2<true>(depth);
-    const float2 p = f2(depth.x < SCAN_NEAR ? -d.m.x : d.a.x, depth.y < SCAN_NEAR ? -d.m.y : d.a.y);
+    const float2 p = scan_p2(depth, scan_decay2<true>(depth));
     return make_float4(cut ? SC_CUT : p.x, cut ? SC_CUT : p.y, b.x, b.y);
 }
 KDA_DEV float2 scan_fold2(float4 v, float2 h) { return scan_step2(f2(v.x, v.y), h, f2(v.z, v.w)); }
@@ -236,12 +239,31 @@ KDA_DEV void store2_odd(void* base, bool bf16, size_t row, int D, int ch, float2
         if (ch + 1 < D) p[1] = v.y;
     }
 }
-// The decays of a token's channels ch, ch + 1 from global memory (for the few that begin a sequence).
+// A token's step of the gradient, back in time, without its decay's rounding: c from behind the token, then from
+// before it.
+KDA_DEV float2 scan_back(float2 depth, float2 d_h, float2 c) {
+    return scan_step2(scan_p2(depth, scan_decay2<true>(depth)), __fadd2_rn(d_h, c), f2(0.f));
+}
+// The gradient of the initial state (channels ch, ch + 1) of a sequence whose first token is t: c, what comes from behind
+// token t + n - 1, taken back over n tokens without the roundings of decays.  For the few warps in which a sequence begins
+// behind the first token: its decays and d_h are loaded once more, which leaves the others their registers, a token
+// ahead; rolled, as code that is new to an SM takes longer to come than to run.
 template <bool BF16>
-__device__ __noinline__ float2 tile_decay(const void* log_alpha, int64_t ld, int t, int D, int ch) {
-    const size_t i = (size_t)t * ld + ch;
-    const float2 d = scan_depth2(f2(ch < D ? ld_in<BF16>(log_alpha, i) : 0.f, ch + 1 < D ? ld_in<BF16>(log_alpha, i + 1) : 0.f));
-    return scan_decay2<!BF16>(d).a;
+__device__ __noinline__ float2 scan_d_init(const void* log_alpha, int64_t ld, const void* d_h, int64_t ld_dh, int t, int n,
+                                           int D, int ch, float2 c) {
+    size_t at = (size_t)(t + n - 1) * ld + ch, at_dh = (size_t)(t + n - 1) * ld_dh + ch;
+    auto row = [&](const void* base, size_t i) {
+        return f2(ch < D ? ld_in<BF16>(base, i) : 0.f, ch + 1 < D ? ld_in<BF16>(base, i + 1) : 0.f);
+    };
+    float2 l = row(log_alpha, at), g = row(d_h, at_dh);
+#pragma unroll 1
+    for (int i = n; i > 0; --i) {
+        const float2 d = scan_depth2(l), dh = g;
+        at -= ld, at_dh -= ld_dh;
+        if (i > 1) l = row(log_alpha, at), g = row(d_h, at_dh);
+        c = scan_back(d, dh, c);
+    }
+    return c;
 }
 KDA_DEV float2 load2(const float* base, size_t row, int D, int ch) {
     const size_t i = row * D + ch;

@@ -61,3 +61,38 @@ def test_decays_are_not_one_sided(dtype):
     for got, ref in ((h[:, -1], sums[:, -1].exp()), (dx[:, 0], (sums[:, -1] - la[:, 0].double()).exp())):
         mean = float((got.double() / ref - 1).mean())
         assert abs(mean) <= (0.6 if dtype == F32 else 16 * 2.3) * scan_ref.EPS, mean / scan_ref.EPS
+
+
+def slow_channels(D, N, dtype):
+    """Log-decays of -1e-5 to -2e-5, constant per sequence and channel."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    return (-1e-5 * (1 + torch.rand((N, D), generator=g, device="cuda"))).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [[1, 1, 1], [5, 5, 5], [16], [16, 21], [8, 3, 13]], ids=str)
+def test_slow_decay_keeps_its_rate_from_call_to_call(dtype, lens):
+    """Some 10000 tokens a sequence in short packed calls, the state handed on, and back, the gradient handed on: decays of
+    1 - 1e-5 to 1 - 2e-5, whose own rounding would put a rate off by up to 2^-25 in 1e-5, 3e-3 of it (5e-4 of such a
+    state over the channels).  As test_slow_decay_keeps_its_rate: two roundings a token of random sign add
+    up to 2^-24 sqrt(2 T / 3) / sqrt(2), 3.5e-6 of a random walk's size for T = 10000, one more per call at most doubles
+    their number; allowed is six times 2^-24 sqrt(4 T / 3) / sqrt(2) = 5e-6."""
+    D, N, calls = 64, len(lens), 10000 // max(lens)
+    cu = [sum(lens[:n]) for n in range(N + 1)]
+    l = slow_channels(D, N, dtype)
+    la = torch.cat([l[n:n + 1].expand(k, D) for n, k in enumerate(lens)])[None].contiguous()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    xs = torch.randn((calls, 1, cu[-1], D), generator=g, device="cuda").to(dtype)
+    state, grad = None, None
+    for c in range(calls):
+        state = kda.scan_fwd(xs[c], la, state, cu_seqlens=as_cu(cu))[1]
+    zero = torch.zeros_like(la)
+    for c in range(calls):
+        grad = kda.scan_bwd(zero, la, xs[calls - 1 - c], None, grad, cu_seqlens=as_cu(cu))["d_initial_state"]
+    for n, k in enumerate(lens):
+        x = xs[:, 0, cu[n]:cu[n + 1]].reshape(calls * k, D).double()
+        ago = torch.arange(calls * k, device="cuda", dtype=torch.float64)[:, None]
+        fwd = (x * torch.exp(ago.flip(0) * l[n].double())).sum(0)
+        bwd = (x * torch.exp((ago + 1) * l[n].double())).sum(0)
+        for got, ref in ((state[n], fwd), (grad[n], bwd)):
+            assert float((got.double() - ref).norm() / ref.norm()) < 3e-5, (n, k)
