@@ -509,7 +509,11 @@ KDA_API kda_status kda_gate_norm_bwd_workspace_size(int64_t rows, int dv, size_t
  *   page_bytes    a positive multiple of 4; pools 16-byte aligned
  *   *_layer_bytes distance between layers (layers == 1: ignored); a multiple of
  *                 4, at least n_pages * page_bytes
- *   dst_slots, src_slots   device int32 [n]
+ *   dst_slots, src_slots   device int32 [n], n at most 65535 (as is layers; KDA_ERR_UNSUPPORTED
+ *                 above): pass a longer list in pieces, one call behind the other
+ *
+ * Entries that read or write a page which another entry writes are carried out one after the
+ * other, all others side by side.
  */
 KDA_API kda_status kda_state_copy(void* dst, const void* src, int layers, int64_t page_bytes, int dst_pages,
                                   int src_pages, int64_t dst_layer_bytes, int64_t src_layer_bytes,
@@ -527,7 +531,8 @@ KDA_API kda_status kda_state_free(uint8_t* live, int n_pages, const int32_t* slo
  * kda_state_compact -- plans the moves that bring all live pages to the front of
  * the pool: with m live pages, the k-th free slot below m receives the k-th live
  * page at or above m.  The moves themselves are kda_state_copy(dst_slots,
- * src_slots, n = n_pages) for each pool that shares the slots.
+ * src_slots, n = n_pages) for each pool that shares the slots, of which the first n_pages / 2
+ * entries hold every move.
  *
  *   live       [n_pages] bytes, on return 1 for the first m and 0 behind them
  *   dst_slots, src_slots  int32 [n_pages]: the moves, then -1

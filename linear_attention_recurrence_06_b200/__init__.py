@@ -38,6 +38,7 @@ KDA_OK = 0
 KDA_F32, KDA_BF16 = 0, 1
 HEAD_DIM = 128
 SCAN_CHUNK = 8  # tokens between two rows of scan_fwd's chunk_states
+COPY_LIST = 65535  # page moves that one kda_state_copy takes
 
 _STATUS_NAMES = {
     0: "KDA_OK", -1: "KDA_ERR_INVALID_ARG", -2: "KDA_ERR_UNSUPPORTED", -3: "KDA_ERR_MISALIGNED",
@@ -848,10 +849,12 @@ def state_copy(dst, dst_slots, src, src_slots, *, layered: bool = False, stream=
         _, Q, _, s_layer = _pool_dims(src, layered, "src")
     if page == 0:
         return dst
-    st = load_library().kda_state_copy(_at(dst), _at(src), L, page, P, Q, d_layer, s_layer, _at(dst_slots),
-                                       _at(src_slots), dst_slots.numel(), _here(dst.get_device()))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_state_copy")
+    lib, n, here = load_library(), dst_slots.numel(), _here(dst.get_device())
+    for at in range(0, n, COPY_LIST):  # longer lists in pieces, one behind the other
+        d, s = (dst_slots, src_slots) if n <= COPY_LIST else (v[at:at + COPY_LIST] for v in (dst_slots, src_slots))
+        st = lib.kda_state_copy(_at(dst), _at(src), L, page, P, Q, d_layer, s_layer, _at(d), _at(s), d.numel(), here)
+        if st != KDA_OK:
+            raise KdaError(st, "kda_state_copy")
     return dst
 
 
