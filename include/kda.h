@@ -445,7 +445,8 @@ KDA_API kda_status kda_scan_bwd_workspace_size(int B, int64_t T, int D, size_t* 
  * place (one token per sequence: n_steps = 1).
  *
  *   state        [n_slots, D] fp32: row slots[b] is sequence b's state; slots
- *                NULL: row b (n_slots >= Bd).  Updated in place.
+ *                NULL: row b (n_slots >= Bd).  Updated in place.  May be NULL
+ *                with slots and n_slots = 0 (every row is padding).
  *   x, log_alpha, gate  [n_steps, Bd, D] in_dtype contiguous, gate or NULL
  *   h            [n_steps, Bd, D] out_dtype
  *   slots        device int32 [Bd] or NULL.  A negative slot, or one of n_slots

@@ -310,7 +310,8 @@ static kda_status decode_steps_impl(float* state, const int32_t* slots, int n_sl
                                     int Bd, int H, int dk, int dv, kda_dtype in_dtype, kda_dtype out_dtype,
                                     float scale, const void* gate, const float* norm_weight, float eps,
                                     float* step_states, void* stream) {
-    if (!state || !q || !k || !v || !log_alpha || !beta || !o) return KDA_ERR_INVALID_ARG;
+    const bool no_pages = slots && n_slots == 0;  // all rows are padding
+    if ((!state && !no_pages) || !q || !k || !v || !log_alpha || !beta || !o) return KDA_ERR_INVALID_ARG;
     if (n_steps < 0 || Bd < 0 || H <= 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype) || eps < 0.f)
         return KDA_ERR_INVALID_ARG;
     if (dk != kSupportedD || dv != kSupportedD) return KDA_ERR_UNSUPPORTED;
@@ -498,7 +499,8 @@ kda_status kda_scan_decode_steps(float* state, const void* x, const void* log_al
     if (n_steps < 0 || Bd < 0 || D <= 0 || n_slots < 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype))
         return KDA_ERR_INVALID_ARG;
     if (Bd == 0 || n_steps == 0) return KDA_OK;
-    if (!state || !x || !log_alpha || !h || (!slots && n_slots < Bd)) return KDA_ERR_INVALID_ARG;
+    const bool no_pages = slots && n_slots == 0;  // all rows are padding
+    if ((!state && !no_pages) || !x || !log_alpha || !h || (!slots && n_slots < Bd)) return KDA_ERR_INVALID_ARG;
     if (Bd > 65535 || D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;  // grid y extent
     const void* ptrs[] = {state, x, log_alpha, gate, h, step_states};
     for (const void* p : ptrs)

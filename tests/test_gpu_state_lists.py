@@ -97,3 +97,18 @@ def test_compaction_of_a_large_pool():
     assert plan["n_live"].item() == m and live[:m].all() and not live[m:].any()
     old = keep.nonzero()[:, 0].cuda()
     assert torch.equal(pool[plan["new_slots"][old].long(), 0].long(), old)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_decode_in_a_pool_without_pages(gated):
+    """Every row is padding: zeros."""
+    n, Bd, H = 2, 3, 2
+    t = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
+    tok = t(n, Bd, H, 128)
+    kw = dict(slots=i32([0, -1, 5]), step_states=True)
+    o, steps = kda.decode_steps(torch.empty((0, H, 128, 128), device="cuda"), tok, tok, tok, tok, t(n, Bd, H),
+                                gate=tok if gated else None, **kw)
+    assert (o == 0).all() and (steps == 0).all()
+    x = t(n, Bd, 40)
+    h, steps = kda.scan_decode_steps(torch.empty((0, 40), device="cuda"), x, x, gate=x if gated else None, **kw)
+    assert (h == 0).all() and (steps == 0).all()
