@@ -483,6 +483,7 @@ def _decode_steps_paged(state, slots, q, k, v, log_alpha, beta, scale, gate, nor
     n, Bd, H, dk = q.shape
     dv = v.shape[-1]
     rows = (n, Bd, H)
+    _check_sizes("kda_decode_steps_paged", n, Bd, H, state.shape[0])
     _check_like(q, torch.float32, (state.shape[0], H, dk, dv), "state", state)
     _check_slots(q, slots, "slots", Bd)
     for t, shape, name in ((k, rows + (dk,), "k"), (v, rows + (dv,), "v"), (log_alpha, rows + (dk,), "log_alpha"),
@@ -551,6 +552,12 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _check_sizes(what, *sizes):
+    """Sizes that the library takes in 32 bits (ctypes would cut them silently)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise KdaError(-2, what)
+
+
 def _check_like(x, dtype, shape, name, t):
     """t: None, or a contiguous tensor of this dtype and shape on x's device."""
     if t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.get_device() == x.get_device()):
@@ -574,6 +581,7 @@ def _check_slots(x, slots, name, n=None):
         raise ValueError(f"{name} must be a CUDA tensor on {x.device}")
     if slots.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
+    _check_sizes(name, slots.numel())
     if slots.dim() != 1 or (n is not None and slots.numel() != n) or not slots.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector" + (f" of {n}" if n is not None else ""))
 
@@ -621,7 +629,9 @@ def _scan_dims(x, cu_seqlens, initial_state):
         N = cu_seqlens.numel() - 1
     if initial_state is not None:
         _check_like(x, _torch().float32, (N,) + ch, "initial_state", initial_state)
-    return B, T, ch, math.prod(ch), N
+    D = math.prod(ch)
+    _check_sizes("kda_scan", B, D, N)
+    return B, T, ch, D, N
 
 
 def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = False, cu_seqlens=None, out_dtype=None,
@@ -674,6 +684,7 @@ def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = F
 
 def scan_bwd_workspace_size(B: int, T: int, D: int) -> int:
     """Workspace bytes of scan_bwd without chunk_states."""
+    _check_sizes("kda_scan_bwd_workspace_size", B, D)
     n = ctypes.c_size_t(0)
     st = load_library().kda_scan_bwd_workspace_size(B, T, D, ctypes.byref(n))
     if st != KDA_OK:
@@ -742,6 +753,8 @@ def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False
     _check_like(x, x.dtype, shape, "gate", gate)
     n, Bd = shape[0], shape[1]
     ch, P = tuple(shape[2:]), state.shape[0]
+    D = math.prod(ch)
+    _check_sizes("kda_scan_decode_steps", n, Bd, P, D)
     _check_like(x, torch.float32, (P,) + ch, "state", state)
     _check_slots(x, slots, "slots", Bd)
     h, want = out, step_states is not None
@@ -753,7 +766,7 @@ def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False
         step_states = _empty(x, shape, torch.float32)
     _check_like(x, torch.float32, shape, "step_states", step_states)
     st = load_library().kda_scan_decode_steps(_at(state), _at(x), _at(log_alpha), _at(gate), _at(h), _at(slots), P, n,
-                                              Bd, math.prod(ch), _dt(x), _dt(h), int(normalize), _at(step_states),
+                                              Bd, D, _dt(x), _dt(h), int(normalize), _at(step_states),
                                               _here(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_scan_decode_steps")
@@ -849,6 +862,7 @@ def state_copy(dst, dst_slots, src, src_slots, *, layered: bool = False, stream=
         _, Q, _, s_layer = _pool_dims(src, layered, "src")
     if page == 0:
         return dst
+    _check_sizes("kda_state_copy", L, P, Q)
     lib, n, here = load_library(), dst_slots.numel(), _here(dst.get_device())
     for at in range(0, n, COPY_LIST):  # longer lists in pieces, one behind the other
         d, s = (dst_slots, src_slots) if n <= COPY_LIST else (v[at:at + COPY_LIST] for v in (dst_slots, src_slots))
@@ -863,6 +877,7 @@ def _check_live(live):
     _check_cuda(live)
     if live.dtype not in (torch.uint8, torch.bool) or live.dim() != 1:
         raise TypeError("live must be a vector of uint8 or bool, one per page")
+    _check_sizes("live", live.numel())
 
 
 def state_alloc(live, n: int, *, stream=None):
@@ -870,6 +885,7 @@ def state_alloc(live, n: int, *, stream=None):
     device) and returns them as int32 [n], -1 where no slot was left."""
     torch = _torch()
     _check_live(live)
+    _check_sizes("kda_state_alloc", n)
     there = _elsewhere(live, stream)
     if there is not None:
         with there:

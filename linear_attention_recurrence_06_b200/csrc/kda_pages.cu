@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) state_alloc_kernel(uint8_t* live
 }
 
 __global__ void __launch_bounds__(256) state_free_kernel(uint8_t* live, int P, const int32_t* slots, int n) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;  // beyond 2^31 in the last CTA of the longest lists
+    if (i >= (unsigned)n) return;
     const int s = slots[i];
     if (s >= 0 && s < P) live[s] = 0;
 }
@@ -214,7 +214,7 @@ cudaError_t launch_state_alloc(uint8_t* live, int P, int32_t* slots, int n, cuda
 }
 
 cudaError_t launch_state_free(uint8_t* live, int P, const int32_t* slots, int n, cudaStream_t stream) {
-    state_free_kernel<<<(n + 255) / 256, 256, 0, stream>>>(live, P, slots, n);
+    state_free_kernel<<<((unsigned)n + 255u) / 256u, 256, 0, stream>>>(live, P, slots, n);
     return cudaGetLastError();
 }
 

@@ -112,3 +112,15 @@ def test_decode_in_a_pool_without_pages(gated):
     x = t(n, Bd, 40)
     h, steps = kda.scan_decode_steps(torch.empty((0, 40), device="cuda"), x, x, gate=x if gated else None, **kw)
     assert (h == 0).all() and (steps == 0).all()
+
+
+def test_free_of_the_longest_list():
+    """2^31 - 100 slots (8.6 GB): the last CTA's numbers pass 31 bits."""
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 10 GB")
+    n = (1 << 31) - 100
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slots[-1], slots[0] = 3, 5
+    live = torch.ones(8, dtype=torch.uint8, device="cuda")
+    kda.state_free(live, slots)
+    assert live.tolist() == [1, 1, 1, 0, 1, 0, 1, 1]
