@@ -382,8 +382,10 @@ KDA_API kda_status kda_gate_norm(const void* o, const void* gate, const float* n
  *   workspace    NULL, or a buffer whose first word receives the device status
  *                (kda_query_status): KDA_ERR_DEVICE_ARG when cu_seqlens breaks
  *                these rules.  Such a call reads and writes nothing out of
- *                range; its outputs are undefined.  At least
- *                KDA_STATUS_BYTES when given.
+ *                range; its outputs are undefined.  KDA_ERR_TIMEOUT when a
+ *                bounded wait gave up.  At least KDA_STATUS_BYTES when given.
+ *                Without a workspace both leave no trace: the call returns
+ *                KDA_OK, its outputs are undefined and nothing says so.
  */
 #define KDA_STATUS_BYTES 256u
 
@@ -505,8 +507,11 @@ KDA_API kda_status kda_gate_norm_bwd_workspace_size(int64_t rows, int dv, size_t
  * one page the last stands.  An entry whose destination is negative or not
  * below dst_pages, or whose source is not below src_pages, does nothing.
  *
- *   dst, src      device pools, or the same pool twice; they may not overlap in
- *                 any other way.  src may be NULL when every entry clears.
+ *   dst, src      device pools, or the same pool twice; otherwise their address ranges,
+ *                 from the first layer's first page to the last layer's last, may not
+ *                 overlap, not even where they share no page (page ranges of one wider
+ *                 pool with several layers: KDA_ERR_INVALID_ARG).  src may be NULL when
+ *                 every entry clears.
  *   page_bytes    a positive multiple of 4; pools 16-byte aligned
  *   *_layer_bytes distance between layers (layers == 1: ignored); a multiple of
  *                 4, at least n_pages * page_bytes

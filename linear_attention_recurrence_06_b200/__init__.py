@@ -647,7 +647,8 @@ def scan_fwd(x, log_alpha, initial_state=None, *, gate=None, normalize: bool = F
     rows of tokens behind cu_seqlens[N] are left as they are.
     Returns (h, final_state fp32 [N, D] or None); with chunk_states (True: allocate)
     also those, fp32 [ceil(B T / 8), D], for scan_bwd.  workspace: optional, for
-    query_status."""
+    query_status: without it a cu_seqlens that breaks its rules, or a wait on the device that
+    gave up, leaves undefined outputs and no trace."""
     torch = _torch()
     B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
     there = _elsewhere(x, stream)
@@ -700,7 +701,8 @@ def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=
     scan_fwd(chunk_states=True) returned for the same inputs; without them they are
     computed first.  Returns a dict: dx, dlog_alpha, dgate (x's shape, fp32 or
     out_dtype; dgate None without a gate) and d_initial_state fp32 [N, D] (None when
-    not wanted)."""
+    not wanted).  workspace: as scan_fwd; without chunk_states scan_bwd_workspace_size bytes
+    (None: allocated, then its status word cannot be asked for)."""
     torch = _torch()
     B, T, ch, D, N = _scan_dims(x, cu_seqlens, initial_state)
     there = _elsewhere(x, stream)
@@ -733,11 +735,12 @@ def scan_bwd(x, log_alpha, d_h, initial_state=None, d_final_state=None, *, gate=
 def scan_decode_steps(state, x, log_alpha, *, gate=None, normalize: bool = False, slots=None, out_dtype=None, out=None,
                       step_states=None, stream=None):
     """n consecutive tokens of the element-wise gated scan for Bd sequences.
-    x, log_alpha, gate: [n, Bd, D] ([n, Bd, H, d]); state: fp32 [P, D], updated in
-    place: sequence b's is row slots[b] (int32 [Bd]; None: row b).  A negative slot
-    marks a row of padding (also one of P and above, and one that an earlier row
-    names): its outputs are zeros and no state changes.  step_states: None, True
-    (allocate) or fp32 [n, Bd, D] receiving the state after every token.
+    x, log_alpha, gate: contiguous [n, Bd, D] ([n, Bd, H, d]; the prefill alone takes
+    columns of wider tensors as they lie).  state: fp32 [P, D], updated in place:
+    sequence b's is row slots[b] (int32 [Bd]; None: row b).  A negative slot marks a row
+    of padding (also one of P and above, and one that an earlier row names): its outputs
+    are zeros and no state changes.  step_states: None, True (allocate) or fp32
+    [n, Bd, D] receiving the state after every token.
     Returns h [n, Bd, D], or (h, step_states)."""
     torch = _torch()
     _check_cuda(x)
@@ -842,7 +845,8 @@ def state_copy(dst, dst_slots, src, src_slots, *, layered: bool = False, stream=
     dtype and page shape (or one pool twice); layered: [L, P, ...], the same slots in
     every layer.  Slots are int32 vectors on the device; an entry with a negative
     destination, or a slot out of range, does nothing.  The result is that of carrying
-    the list out one by one.  src None: every entry clears.  Returns dst."""
+    the list out one by one.  src None: every entry clears.  Pools of several layers whose
+    address ranges interleave (two slices of a wider one) are refused.  Returns dst."""
     if not dst.is_cuda or (src is not None and (not src.is_cuda or src.device != dst.device)):
         raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
     _check_slots(dst, dst_slots, "dst_slots")
