@@ -7,8 +7,9 @@
 // room for (those come from shared memory).  d_norm_weight is summed in a fixed order: each lane over
 // the rows of its half warp, a CTA's half warps through shared memory, the CTAs by a second
 // kernel, whose launch overlaps the first's end.
-// 262,144 rows in bf16: 57.4 us, 5.8 TB/s of the 6.5 that a copy reaches (65.3 us without the loads
-// ahead), 2.2 us of it the second kernel; fp32 125 us, 5.4 TB/s; 602 rows: 6.2 us, most of it the two launches.
+// 262,144 rows in bf16: 54 us, 6.2 TB/s of the 6.5 that a copy reaches (8 us more without the loads
+// ahead), 2 us of it the second kernel; fp32 122 us, 5.5 TB/s (592 CTAs where 444 run at once; those kernels spill
+// 28 bytes, bf16 inputs with fp32 gradients 12); 602 rows: 3.6 us, most of it the two launches.
 #include <float.h>
 
 #include "kda_launch.h"

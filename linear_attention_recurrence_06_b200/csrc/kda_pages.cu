@@ -1,8 +1,8 @@
 // kda_pages.cu -- pages of recurrent states (include/kda.h, kda_state_copy,
 // kda_state_alloc, kda_state_free, kda_state_compact).  Copies are HBM-bound: 80
-// pages of 2 MiB take 53 us, 6.3 TB/s of the 6.5 of one plain copy; 8 pages forked into
-// 64 and 8 cleared 31 us (168 MB, 26 us at that rate).  The plans are one CTA: 6 us for 96
-// pages, 15 us for 5,000.
+// pages of 2 MiB take 52 us, 6.4 TB/s of the 6.5 of one plain copy; 8 pages forked into
+// 64 and 8 cleared 28 us (168 MB, 26 us at that rate).  The plans are one CTA: 4 us for 96
+// pages, 14 us for 5,000.
 #include "kda_launch.h"
 #include "kda_sm100.cuh"
 

@@ -35,12 +35,13 @@ namespace {
 // The forward: kda_scan_tile.cuh says how the work is split.  A warp's first run keeps each token's
 // state from zero and the product of the decays up to it; with the state before the warp's
 // tokens known, the second is one fused product per value.  (Those products' rounding stays
-// inside a token's output; what is carried on goes by the sum of the log-decays.)
+// inside a token's output; what is carried on, final states too, goes by the sum of the log-decays.)
 // 16 tokens per warp in bf16: two stages of two CTAs still fit an SM's shared memory, and the hand-overs, which
 // cost as much for 8 tokens, are half as many; the 64 registers of a warp's states and decays are what
-// limits it.  Gated bf16, 4 x 2048 x 4096: 55 us, 4.8 TB/s (without either factor 37 us, 5.5 TB/s; fp32 92 us, 5.8 TB/s; rows
-// of 4094, without TMA, 126 us); one sequence of 8192: 73 us, 3.7 TB/s, of 32,768: 254 us, 4.2 TB/s (clusters of 4);
-// 125,841 tokens in 16 packed sequences: 744 us, 5.5 TB/s.  What bounds it: schedulers that share two CTAs issue in three of four cycles, and 256 such CTAs
+// limits it.  Gated bf16, 4 x 2048 x 4096: 54 us, 5.0 TB/s (without either factor 35 us, 5.7 TB/s; fp32 90 us, 6.0 TB/s; rows
+// of 4094, without TMA, 134 us: copies of 4 bytes, and those kernels spill 140 to 152 bytes); one sequence of 8192: 70 us,
+// 3.8 TB/s, of 32,768: 246 us, 4.4 TB/s (clusters of 4: an exchange per step, schedulers issue in 46 % of cycles);
+// 110,842 tokens in 16 packed sequences: 685 us, 5.3 TB/s.  What bounds it: schedulers that share two CTAs issue in three of four cycles, and 256 such CTAs
 // leave 40 of 148 SMs with one.
 template <bool BF16, bool GATE>
 struct ScanFwd {
@@ -328,8 +329,8 @@ __global__ void scan_check_cu_kernel(const int32_t* cu, int n_seqs, int64_t T, u
 // Single tokens: V channels of one row per thread (4 where D allows 16-byte states), the state read
 // and written once for all steps of a call.  HBM-bound for many rows, else latency: the row's
 // slot, its state and the first tokens are on their way before the slot is checked against the
-// rows before it, and every step's tokens are loaded a step ahead.  256 rows x 4096 through slots: 6.2 us
-// (16.6 MB: 2.5 us at a copy's rate); 3 rows x 1000, five tokens: 4.2 us.
+// rows before it, and every step's tokens are loaded a step ahead.  256 rows x 4096 through slots: 5.0 us
+// (16.6 MB: 2.5 us at a copy's rate); 3 rows x 1000, five tokens: 3.0 us.
 template <bool BF16, int V>
 KDA_DEV void load_v(const void* base, size_t i, float* v) {
     if constexpr (V == 1) {

@@ -8,9 +8,11 @@
 // without it the warps' states would have to be handed on as well, before they could begin to
 // walk back), for the factors; then back from zero.  14.5 bytes per value in bf16.  8 tokens per warp: the three
 // factors, the gradient from zero and the products of the decays of 8 tokens already take the 128 registers.
-// Gated bf16, 4 x 2048 x 4096: 94 us, 5.2 TB/s (without either factor 61 us; fp32 156 us, 6.1 TB/s); one sequence of 8192:
-// 125 us, 3.9 TB/s, of 32,768: 464 us, 4.2 TB/s; 125,841 tokens in 16 packed sequences: 1.41 ms, 5.3 TB/s.  The kept states came
-// by plain loads at first: 114 us for the first case.
+// Gated bf16, 4 x 2048 x 4096: 94 us, 5.2 TB/s (without either factor 60 us; fp32 157 us, 6.1 TB/s; rows of 4094, without
+// TMA, 160 us, gated ones spill 44 to 56 bytes); one sequence of 8192: 127 us, 3.8 TB/s, of 32,768: 476 us, 4.1 TB/s; 110,842
+// tokens in 16 packed sequences: 1.30 ms, 5.1 TB/s.  The kept states came by plain loads at first: 114 us for the first case.
+// Sequences that meet inside a tile cost most: 4,417 tokens in 23 sequences of 0 to 401, x 1000 fp32, take 47 us, 4,416 in 23 of
+// 192 28 us (loads of initial states and of their gradients in the middle of the walk, one CTA per SM to hide them).
 // Bound by issue slots where two CTAs share an SM, as the forward.
 #include <float.h>
 
